@@ -307,6 +307,86 @@ haste_status_t haste_head_backward(int32_t B, int32_t H, int32_t d, haste_dtype_
                                    const void* Wh, const void* dY_h, void* dWh, float* dXh, void* ws,
                                    size_t ws_bytes, haste_stream_t stream);
 
+/* ------------------------------------------------- dense head in 8 bits --- */
+
+/* Row-wise symmetric quantisation to 8-bit integers, one scale per row (per label
+ * for weights Wh [H, d], per sample for features Xh [B, d]):
+ *   scale[r] = max_j |x[r, j]| / 127, rounded once to fp32;
+ *   q[r, j]  = x[r, j] / scale[r] (the exact quotient), rounded half to even and
+ *              kept within +-127; 0 where scale[r] is 0.
+ * A row that holds a NaN or an infinity gets the scale NaN and q = 0.
+ *   x      device [rows, n] in dtype, contiguous
+ *   q      device int8 [rows, haste_i8_pitch(n)], 16-byte aligned; the columns
+ *          from n on are set to 0
+ *   scale  device fp32 [rows]
+ * Supported: 1 <= n <= 131072 (the products' sums then fit 32 bits).  The paper
+ * has no counterpart: 8-bit scoring is this library's, for serving the dense
+ * classifier of Methodology 2 at half the weight bytes. */
+int32_t haste_i8_pitch(int32_t n); /* n rounded up to a multiple of 16; 0 for n <= 0 */
+haste_status_t haste_quantize_rows(int64_t rows, int32_t n, haste_dtype_t dtype, const void* x, int8_t* q,
+                                   float* scale, haste_stream_t stream);
+
+/* Workspace bytes of haste_head_forward_i8 at (B, H, d): the quantised features. */
+size_t haste_head_i8_workspace_size(int32_t B, int32_t H, int32_t d);
+
+/* Dense head logits from 8-bit weights, for scoring: the rows of Xh are quantised
+ * (as haste_quantize_rows) within the call, and
+ *   logits[b, h] = (float)(sum_f qx[b, f] * Wq[h, f]) * (sx[b] * w_scale[h]),
+ * the sum exact in 32-bit integers on the tensor cores, the logits rounded to
+ * out_dtype.  A sample with a NaN or an infinity gets NaN logits.
+ *   Xh      device [B, d] in dtype;  Wq device int8 [H, haste_i8_pitch(d)],
+ *   16-byte aligned, and w_scale device fp32 [H], from haste_quantize_rows
+ *   logits  device [B, H] in out_dtype (fp32 logits keep what haste_logprob reads)
+ * Supported: d <= 131072, any B and H. */
+haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtype_t dtype, const void* Xh,
+                                     const int8_t* Wq, const float* w_scale, haste_dtype_t out_dtype, void* logits,
+                                     void* ws, size_t ws_bytes, haste_stream_t stream);
+
+/* ------------------------------------------------- softmax of the logits --- */
+
+/* Workspace bytes of haste_logprob at (B, N, k). */
+size_t haste_logprob_workspace_size(int32_t B, int64_t N, haste_dtype_t dtype, int32_t k);
+
+/* Log probabilities of given labels, entropy and the k best alternatives, from
+ * logits [B, N] of any layer of this library (haste_forward, haste_head_forward,
+ * haste_head_forward_i8), read as a softmax over each sample's N labels:
+ *   lse[b] = log sum_j e^z[b, j];  log p[b, j] = z[b, j] - lse[b];
+ *   logp[i] = log p[b, ids[i]] for row_ptr[b] <= i < row_ptr[b + 1];
+ *   entropy[b] = -sum_j p[b, j] log p[b, j];
+ *   top_id [B, k], top_logp [B, k]: the k labels of the largest logits and their
+ *   log p, larger logit first, equal logits by smaller label id.
+ * All sums are held in fp32.  A masked label has the logit -inf: p = 0, log p =
+ * -inf, no entropy.  A row of nothing but -inf has lse = log p = -inf and entropy
+ * 0; a row with a NaN or +inf gets NaN throughout (its top_id ranks a NaN as -inf).
+ *   logits    device [B, N] in dtype, contiguous
+ *   given     row_ptr [B + 1] and ids [nnz]; unlike elsewhere the ids of a row may
+ *             come in any order and repeat, and an id outside [0, N) gets NaN.
+ *             row_ptr NULL: none (ids and logp are not read).  Entries of row_ptr
+ *             are kept within [0, nnz]; logp [nnz] outside them is left as it was.
+ *   lse, entropy  fp32 [B], each may be NULL;  logp fp32 [nnz]
+ *   k         0 <= k <= min(64, N); top_logp and top_id may be NULL when k = 0
+ * Supported: 1 <= N < 2^31.  The paper names no loss; the softmax reading, next to
+ * the BCE of the fused steps, is this library's. */
+haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dtype, const void* logits, haste_targets_t given,
+                             int64_t nnz, int32_t k, float* logp, float* lse, float* entropy, float* top_logp,
+                             int32_t* top_id, void* ws, size_t ws_bytes, haste_stream_t stream);
+
+/* Gradient of haste_logprob's logp and entropy with respect to the logits:
+ *   d_logits[b, j] = sum over row b's i with ids[i] = j of d_logp[i]
+ *                    - p[b, j] * (G[b] + d_entropy[b] * (log p[b, j] + entropy[b])),
+ *   G[b] = sum of row b's d_logp,
+ * in the logits' dtype, ready for haste_head_backward, haste_backward_dw and
+ * haste_backward_dx.  lse and entropy are haste_logprob's.  Masked labels get 0
+ * (and their own d_logp where they are given); rows of nothing but -inf get 0;
+ * ids outside [0, N) count for nothing.  The choice of alternatives (top_*) has no
+ * gradient.  The sums run in the order of the lists: repeats give the same bits.
+ *   given.row_ptr NULL: no logp term.  d_entropy NULL: no entropy term (entropy is
+ *   not read).  d_logits must not overlap logits. */
+haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dtype, const void* logits,
+                                      const float* lse, const float* entropy, haste_targets_t given, int64_t nnz,
+                                      const float* d_logp, const float* d_entropy, void* d_logits,
+                                      haste_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

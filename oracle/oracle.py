@@ -14,7 +14,8 @@ reading; the page names no loss.
 
 Functions return float64 arrays.  bf16 inputs are uint16 bit patterns and widen
 exactly.  Parity status: every function here is pinned by ``tests/test_oracle.py``
-(dense masked products, brute-force loops, finite differences, closed forms).
+and ``tests/test_softmax_i8_host.py`` (dense masked products, brute-force loops,
+finite differences, closed forms, rational arithmetic).
 """
 from __future__ import annotations
 
@@ -275,3 +276,83 @@ def head_step(Xh, Wh, row_ptr, ids, scale: float):
     loss, dY = bce(z, row_ptr, ids, scale)
     dWh, dXh = head_backward(Xh, Wh, dY)
     return loss, dY, dWh, dXh
+
+
+# ------------------------------------------------------- dense head in 8 bits
+def quantize_rows(x) -> Tuple[np.ndarray, np.ndarray]:
+    """(q int64 [rows, n], scale float32 [rows]): scale = max|x| / 127 rounded once to
+    fp32, q = x / scale rounded half to even within +-127 (0 where scale is 0); a
+    row with a NaN or an infinity has scale NaN and q = 0.  The fp64 quotient of
+    two fp32 numbers of which one is at most about 127 times the other lies on the
+    same side of every half as the exact one, so rint is exact."""
+    x = to_f64(np.asarray(x))
+    amax = np.abs(x).max(axis=1)
+    ok = np.isfinite(amax)
+    scale = np.where(ok, np.where(ok, amax, 0.0) / 127.0, np.nan).astype(np.float32)
+    s = scale.astype(np.float64)[:, None]
+    live = ok[:, None] & (s > 0)
+    q = np.rint(np.divide(x, s, out=np.zeros_like(x), where=live))
+    return np.clip(q, -127, 127).astype(np.int64), scale
+
+
+def head_forward_i8(Xh, Wq, w_scale) -> np.ndarray:
+    """Head logits of features quantised per sample against 8-bit weights Wq [H, d]
+    (whole numbers) with the fp32 scale w_scale [H] of each label."""
+    q, sx = quantize_rows(Xh)
+    acc = q.astype(np.float64) @ np.asarray(Wq, dtype=np.float64).T  # whole numbers below 2^53: exact
+    return acc * (sx.astype(np.float64)[:, None] * np.asarray(w_scale, dtype=np.float64)[None, :])
+
+
+# ------------------------------------------------------- softmax of the logits
+def logprob(logits, row_ptr, ids, k: int):
+    """(logp [nnz], lse [B], entropy [B], top_logp [B, k], top_id [B, k]) of logits
+    [B, N] in fp64.  -inf logits are masked labels; a row of nothing else has lse =
+    log p = -inf and entropy 0; a row with a NaN or +inf is NaN throughout (its
+    alternatives rank a NaN as -inf).  Ids outside [0, N) get NaN."""
+    z = to_f64(np.asarray(logits))
+    B, N = z.shape
+    lse, entropy = np.empty(B), np.empty(B)
+    logp_out = np.full(len(ids), np.nan)
+    top_logp, top_id = np.empty((B, k)), np.empty((B, k), dtype=np.int64)
+    for b in range(B):
+        r = z[b]
+        m = np.max(r)
+        if np.isnan(m) or m == np.inf:
+            lse[b] = entropy[b] = np.nan
+            logp = np.full(N, np.nan)
+        elif m == -np.inf:
+            lse[b], entropy[b] = -np.inf, 0.0
+            logp = np.full(N, -np.inf)
+        else:
+            e = np.exp(r - m)
+            lse[b] = m + np.log(e.sum())
+            logp = r - lse[b]
+            p = np.exp(logp)
+            entropy[b] = -np.sum(p * np.where(p > 0, logp, 0.0))
+        rank = np.argsort(-np.where(np.isnan(r), -np.inf, r), kind="stable")[:k]
+        top_id[b], top_logp[b] = rank, logp[rank]
+        for i in range(row_ptr[b], row_ptr[b + 1]):
+            if 0 <= ids[i] < N:
+                logp_out[i] = logp[ids[i]]
+    return logp_out, lse, entropy, top_logp, top_id
+
+
+def logprob_backward(logits, row_ptr, ids, d_logp, d_entropy=None) -> np.ndarray:
+    """d_logits [B, N] in fp64: the given labels' d_logp, less p (their row's sum +
+    d_entropy (log p + entropy)).  Rows of nothing but -inf get 0."""
+    z = to_f64(np.asarray(logits))
+    B, N = z.shape
+    out = np.zeros((B, N))
+    _, lse, entropy, _, _ = logprob(logits, np.zeros(B + 1, np.int64), [], 0)
+    for b in range(B):
+        if lse[b] == -np.inf:
+            continue
+        logp = z[b] - lse[b]
+        p = np.exp(logp)
+        mine = [i for i in range(row_ptr[b], row_ptr[b + 1]) if 0 <= ids[i] < N]
+        c = float(sum(float(d_logp[i]) for i in mine))
+        gh = 0.0 if d_entropy is None else float(d_entropy[b])
+        out[b] = -p * (c + gh * (np.where(p > 0, logp, 0.0) + entropy[b]))
+        for i in mine:
+            out[b, ids[i]] += float(d_logp[i])
+    return out

@@ -23,6 +23,8 @@
 #include "tail_given.cu"
 #include "topk.cu"
 #include "plan.cu"
+#include "head_i8.cu"
+#include "logprob.cu"
 
 using namespace haste;
 
@@ -1040,6 +1042,146 @@ haste_status_t haste_head_backward(int32_t B, int32_t H, int32_t d, haste_dtype_
                          : head::backward_dx<float>(B, H, d, Wh, dYh, dXh, part, s);
   }
   return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_head_backward launch");
+}
+
+// ---------------------------------------------------------- head in 8 bits
+// Workspace of haste_head_forward_i8: the quantised features and their scales.
+static size_t head_i8_ws(int B, int d, size_t* scale) {
+  *scale = align256((size_t)B * head8::pitch(d));
+  return *scale + align256((size_t)B * 4);
+}
+
+static haste_status_t check_i8(int d, haste_dtype_t dt) {
+  if (dt != HASTE_F32 && dt != HASTE_BF16) return fail(HASTE_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+  if (d > head8::kMaxN)
+    return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "%d columns: sums of 8-bit products fit 32 bits up to %d", d, head8::kMaxN);
+  return HASTE_OK;
+}
+
+// A tensor's address must be a multiple of its element (or vector) size.
+static haste_status_t check_aligned(const void* p, size_t bytes, const char* name) {
+  if (reinterpret_cast<uintptr_t>(p) % bytes)
+    return fail(HASTE_ERR_INVALID_ARG, "%s must be aligned to %zu bytes", name, bytes);
+  return HASTE_OK;
+}
+
+int32_t haste_i8_pitch(int32_t n) { return n <= 0 || n > 0x7ffffff0 ? 0 : head8::pitch(n); }
+
+haste_status_t haste_quantize_rows(int64_t rows, int32_t n, haste_dtype_t dt, const void* x, int8_t* q, float* scale,
+                                   haste_stream_t stream) {
+  haste_status_t st = check_i8(n, dt);
+  if (st != HASTE_OK) return st;
+  if (rows <= 0 || rows > 0x7fffffff || n <= 0)
+    return fail(HASTE_ERR_INVALID_ARG, "rows and n must be positive, rows below 2^31");
+  if (!x || !q || !scale) return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
+  if ((st = check_aligned(x, elem_bytes(dt), "x")) != HASTE_OK) return st;
+  if ((st = check_aligned(q, 16, "q")) != HASTE_OK) return st;
+  if ((st = check_aligned(scale, 4, "scale")) != HASTE_OK) return st;
+  DeviceInfo di;
+  if ((st = device_info(di)) != HASTE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps("quantize_rows", s);
+  const cudaError_t e = dt == HASTE_BF16 ? head8::launch_quantize<__nv_bfloat16>(rows, n, x, q, scale, s)
+                                         : head8::launch_quantize<float>(rows, n, x, q, scale, s);
+  return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_quantize_rows launch");
+}
+
+size_t haste_head_i8_workspace_size(int32_t B, int32_t H, int32_t d) {
+  if (B <= 0 || H <= 0 || d <= 0 || d > head8::kMaxN) return 0;
+  size_t scale;
+  return head_i8_ws(B, d, &scale);
+}
+
+haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtype_t dt, const void* Xh,
+                                     const int8_t* Wq, const float* w_scale, haste_dtype_t out_dt, void* logits,
+                                     void* ws, size_t ws_bytes, haste_stream_t stream) {
+  haste_status_t st = check_i8(d, dt);
+  if (st == HASTE_OK) st = check_i8(d, out_dt);
+  if (st != HASTE_OK) return st;
+  if (B <= 0 || H <= 0 || d <= 0) return fail(HASTE_ERR_INVALID_ARG, "B, H and d must be positive");
+  if (!Xh || !Wq || !w_scale || !logits) return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
+  if ((st = check_aligned(Xh, elem_bytes(dt), "Xh")) != HASTE_OK) return st;
+  if ((st = check_aligned(Wq, 16, "Wq")) != HASTE_OK) return st;
+  if ((st = check_aligned(w_scale, 4, "w_scale")) != HASTE_OK) return st;
+  if ((st = check_aligned(logits, elem_bytes(out_dt), "logits")) != HASTE_OK) return st;
+  size_t sc;
+  const size_t need = head_i8_ws(B, d, &sc);
+  if ((st = check_ws(ws, ws_bytes, need)) != HASTE_OK) return st;
+  if ((st = check_aligned(ws, 16, "the workspace")) != HASTE_OK) return st;
+  DeviceInfo di;
+  if ((st = device_info(di)) != HASTE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int8_t* qx = static_cast<int8_t*>(ws);
+  float* sx = reinterpret_cast<float*>(qx + sc);
+  cudaError_t e;
+  {
+    ProfScope ps("quantize_rows", s);
+    e = dt == HASTE_BF16 ? head8::launch_quantize<__nv_bfloat16>(B, d, Xh, qx, sx, s)
+                         : head8::launch_quantize<float>(B, d, Xh, qx, sx, s);
+  }
+  if (e == cudaSuccess) {
+    ProfScope ps("head_forward_i8", s);
+    const int ld = head8::pitch(d);
+    e = out_dt == HASTE_BF16 ? head8::launch_product<__nv_bfloat16>(B, H, ld, qx, sx, Wq, w_scale, logits, s)
+                             : head8::launch_product<float>(B, H, ld, qx, sx, Wq, w_scale, logits, s);
+  }
+  return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_head_forward_i8 launch");
+}
+
+// ---------------------------------------------------- softmax of the logits
+static haste_status_t check_logprob(int B, int64_t N, haste_dtype_t dt, const haste_targets_t& given, int64_t nnz) {
+  if (dt != HASTE_F32 && dt != HASTE_BF16) return fail(HASTE_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+  if (B <= 0 || N <= 0) return fail(HASTE_ERR_INVALID_ARG, "B and N must be positive");
+  if (N > 0x7fffffff) return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "N=%lld: label ids are 32-bit", (long long)N);
+  if (nnz < 0 || nnz > 0x7fffffff) return fail(HASTE_ERR_INVALID_ARG, "nnz=%lld out of [0, 2^31)", (long long)nnz);
+  if (nnz > 0 && !given.row_ptr) return fail(HASTE_ERR_INVALID_ARG, "given ids need their row_ptr");
+  if (nnz > 0 && !given.ids) return fail(HASTE_ERR_INVALID_ARG, "ids is NULL");
+  return HASTE_OK;
+}
+
+size_t haste_logprob_workspace_size(int32_t B, int64_t N, haste_dtype_t dt, int32_t k) { return 0; }
+
+haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void* logits, haste_targets_t given,
+                             int64_t nnz, int32_t k, float* logp, float* lse, float* entropy, float* top_logp,
+                             int32_t* top_id, void* ws, size_t ws_bytes, haste_stream_t stream) {
+  haste_status_t st = check_logprob(B, N, dt, given, nnz);
+  if (st != HASTE_OK) return st;
+  if (k < 0 || k > 64 || k > N) return fail(HASTE_ERR_INVALID_ARG, "k=%d must lie in [0, min(64, N)]", k);
+  if (!logits || (nnz > 0 && !logp) || (k > 0 && (!top_logp || !top_id)))
+    return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
+  if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, haste_logprob_workspace_size(B, N, dt, k))) != HASTE_OK) return st;
+  DeviceInfo di;
+  if ((st = device_info(di)) != HASTE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  logprob::Args a{logits, N, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, k, logp, lse, entropy, top_logp, top_id};
+  ProfScope ps("logprob", s);
+  const cudaError_t e = dt == HASTE_BF16 ? logprob::launch<__nv_bfloat16>(B, a, s) : logprob::launch<float>(B, a, s);
+  return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_logprob launch");
+}
+
+haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dt, const void* logits, const float* lse,
+                                      const float* entropy, haste_targets_t given, int64_t nnz, const float* d_logp,
+                                      const float* d_entropy, void* d_logits, haste_stream_t stream) {
+  haste_status_t st = check_logprob(B, N, dt, given, nnz);
+  if (st != HASTE_OK) return st;
+  if (!logits || !lse || !d_logits || (nnz > 0 && !d_logp)) return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (d_entropy && !entropy) return fail(HASTE_ERR_INVALID_ARG, "d_entropy needs the entropies");
+  if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
+  if ((st = check_aligned(d_logits, elem_bytes(dt), "d_logits")) != HASTE_OK) return st;
+  const uintptr_t za = reinterpret_cast<uintptr_t>(logits), ga = reinterpret_cast<uintptr_t>(d_logits);
+  const uintptr_t bytes = (uintptr_t)B * (uintptr_t)N * elem_bytes(dt);
+  if (za < ga + bytes && ga < za + bytes)
+    return fail(HASTE_ERR_INVALID_ARG, "d_logits must not overlap logits: given labels are read after the dense pass");
+  DeviceInfo di;
+  if ((st = device_info(di)) != HASTE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  logprob::GradArgs a{logits, N, lse, entropy, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, d_logp, d_entropy,
+                      d_logits};
+  ProfScope ps("logprob_backward", s);
+  const cudaError_t e =
+      dt == HASTE_BF16 ? logprob::launch_grad<__nv_bfloat16>(B, a, s) : logprob::launch_grad<float>(B, a, s);
+  return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_logprob_backward launch");
 }
 
 }  // extern "C"

@@ -85,6 +85,13 @@ def lib() -> ctypes.CDLL:
         "haste_head_workspace_size": ([I32, I32, I32, S], SZ),
         "haste_head_forward": ([I32, I32, I32, S, P, P, P, P, F, P, P, SZ, P], S),
         "haste_head_backward": ([I32, I32, I32, S, P, P, P, P, P, P, SZ, P], S),
+        "haste_i8_pitch": ([I32], I32),
+        "haste_quantize_rows": ([I64, I32, S, P, P, P, P], S),
+        "haste_head_i8_workspace_size": ([I32, I32, I32], SZ),
+        "haste_head_forward_i8": ([I32, I32, I32, S, P, P, P, S, P, P, SZ, P], S),
+        "haste_logprob_workspace_size": ([I32, I64, S, I32], SZ),
+        "haste_logprob": ([I32, I64, S, P, Targets, I64, I32, P, P, P, P, P, P, SZ, P], S),
+        "haste_logprob_backward": ([I32, I64, S, P, P, P, Targets, I64, P, P, P, P], S),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -407,3 +414,115 @@ def haste_head_backward(Xh, Wh, dYh, dWh, dXh, ws, stream=None) -> None:
     p, n = _ws(ws)
     _check(lib().haste_head_backward(B, H, d, dtype_code(Xh), _tptr(Xh), _tptr(Wh), _tptr(dYh), _tptr(dWh),
                                      _tptr(dXh), p, n, _stream(stream)), "haste_head_backward")
+
+
+def _current_device(**tensors):
+    """Every tensor on the current CUDA device: the calls below launch there."""
+    import torch
+    _same_device(None, **tensors)
+    dev = next(t.device for t in tensors.values() if t is not None)
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, but cuda:{torch.cuda.current_device()} is current")
+
+
+# ------------------------------------------------------- dense head in 8 bits
+def haste_i8_pitch(n: int) -> int:
+    """Columns of a quantised row of n values (n rounded up to 16)."""
+    return int(lib().haste_i8_pitch(n))
+
+
+def haste_quantize_rows(x, q, scale, stream=None) -> None:
+    """Row-wise 8-bit quantisation of x [rows, n]: q int8 [rows, haste_i8_pitch(n)]
+    and scale fp32 [rows] (see include/haste.h)."""
+    import torch
+    rows, n = x.shape
+    code = dtype_code(x)
+    _expect(q, "q", (rows, haste_i8_pitch(n)), torch.int8)
+    _expect(scale, "scale", (rows,), torch.float32)
+    _current_device(x=x, q=q, scale=scale)
+    _check(lib().haste_quantize_rows(rows, n, code, _tptr(x), _tptr(q), _tptr(scale), _stream(stream)),
+           "haste_quantize_rows")
+
+
+def haste_head_i8_workspace_size(B: int, H: int, d: int) -> int:
+    return int(lib().haste_head_i8_workspace_size(B, H, d))
+
+
+def haste_head_forward_i8(Xh, Wq, w_scale, logits, ws, stream=None) -> None:
+    """Head logits [B, H] (fp32 or bf16) from 8-bit weights Wq [H, haste_i8_pitch(d)]
+    with a scale per label; Xh [B, d] is quantised per sample within the call."""
+    import torch
+    B, d = Xh.shape
+    H = Wq.shape[0]
+    code, out_code = dtype_code(Xh), dtype_code(logits)
+    _expect(Wq, "Wq", (H, haste_i8_pitch(d)), torch.int8)
+    _expect(w_scale, "w_scale", (H,), torch.float32)
+    _expect(logits, "logits", (B, H))
+    _current_device(Xh=Xh, Wq=Wq, w_scale=w_scale, logits=logits, ws=ws)
+    p, n = _ws(ws)
+    _check(lib().haste_head_forward_i8(B, H, d, code, _tptr(Xh), _tptr(Wq), _tptr(w_scale), out_code, _tptr(logits),
+                                       p, n, _stream(stream)), "haste_head_forward_i8")
+
+
+# ------------------------------------------------------- softmax of the logits
+def _given(row_ptr, ids, B: int, per_id, per_id_name: str) -> int:
+    """The given labels' lists (both or neither) and their fp32 values; returns nnz."""
+    import torch
+    if row_ptr is None:
+        if ids is not None or per_id is not None:
+            raise ValueError(f"ids and {per_id_name} need the given labels' row_ptr")
+        return 0
+    _targets(row_ptr, ids, B, "given")
+    _expect(per_id, per_id_name, (ids.numel(),), torch.float32)
+    return ids.numel()
+
+
+def haste_logprob_workspace_size(B: int, N: int, dtype: int, k: int) -> int:
+    return int(lib().haste_logprob_workspace_size(B, N, dtype, k))
+
+
+def haste_logprob(logits, row_ptr=None, ids=None, logp=None, lse=None, entropy=None, top_logp=None, top_id=None,
+                  ws=None, stream=None) -> None:
+    """Softmax reading of logits [B, N] (see include/haste.h): log p of the given
+    labels (row_ptr [B + 1], ids and logp [nnz]), lse and entropy [B], and the
+    alternatives top_logp and top_id [B, k]; outputs that are None are not computed."""
+    import torch
+    B, N = logits.shape
+    code = dtype_code(logits)
+    nnz = _given(row_ptr, ids, B, logp, "logp")
+    for n, t in (("lse", lse), ("entropy", entropy)):
+        if t is not None:
+            _expect(t, n, (B,), torch.float32)
+    k = 0
+    if top_id is not None or top_logp is not None:
+        if top_id is None or top_logp is None:
+            raise ValueError("top_logp and top_id come together")
+        k = top_id.shape[-1]
+        _expect(top_id, "top_id", (B, k), torch.int32)
+        _expect(top_logp, "top_logp", (B, k), torch.float32)
+    _current_device(logits=logits, row_ptr=row_ptr, ids=ids, logp=logp, lse=lse, entropy=entropy, top_logp=top_logp,
+                    top_id=top_id, ws=ws)
+    p, n = _ws(ws)
+    _check(lib().haste_logprob(B, N, code, _tptr(logits), Targets(_tptr(row_ptr), _tptr(ids)), nnz, k, _tptr(logp),
+                               _tptr(lse), _tptr(entropy), _tptr(top_logp), _tptr(top_id), p, n, _stream(stream)),
+           "haste_logprob")
+
+
+def haste_logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy, d_logits, stream=None) -> None:
+    """Gradient of haste_logprob's logp and entropy in the logits: d_logits [B, N] in
+    their dtype.  row_ptr, ids and d_logp may be None together (no logp term), and
+    d_entropy may be None (no entropy term; entropy is then not read)."""
+    import torch
+    B, N = logits.shape
+    code = dtype_code(logits)
+    nnz = _given(row_ptr, ids, B, d_logp, "d_logp")
+    _expect(lse, "lse", (B,), torch.float32)
+    for n, t in (("entropy", entropy), ("d_entropy", d_entropy)):
+        if t is not None or (n == "entropy" and d_entropy is not None):
+            _expect(t, n, (B,), torch.float32)
+    _expect(d_logits, "d_logits", (B, N), logits.dtype)
+    _current_device(logits=logits, lse=lse, entropy=entropy, row_ptr=row_ptr, ids=ids, d_logp=d_logp,
+                    d_entropy=d_entropy, d_logits=d_logits)
+    _check(lib().haste_logprob_backward(B, N, code, _tptr(logits), _tptr(lse), _tptr(entropy),
+                                        Targets(_tptr(row_ptr), _tptr(ids)), nnz, _tptr(d_logp), _tptr(d_entropy),
+                                        _tptr(d_logits), _stream(stream)), "haste_logprob_backward")
