@@ -1048,7 +1048,7 @@ haste_status_t haste_head_backward(int32_t B, int32_t H, int32_t d, haste_dtype_
 // Workspace of haste_head_forward_i8: the quantised features and their scales.
 static size_t head_i8_ws(int B, int d, size_t* scale) {
   *scale = align256((size_t)B * head8::pitch(d));
-  return *scale + align256((size_t)B * 4);
+  return *scale + align256((size_t)B * 4) + 1024;  // the product's tiles read the scales in whole tiles of 256
 }
 
 static haste_status_t check_i8(int d, haste_dtype_t dt) {
@@ -1099,6 +1099,8 @@ haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtyp
   if (st == HASTE_OK) st = check_i8(d, out_dt);
   if (st != HASTE_OK) return st;
   if (B <= 0 || H <= 0 || d <= 0) return fail(HASTE_ERR_INVALID_ARG, "B, H and d must be positive");
+  if (B > head8::kMaxBH || H > head8::kMaxBH || head8::max_tiles(B, H) > 0x7fffffff)
+    return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "B=%d, H=%d: more tiles than 32-bit indices count", B, H);
   if (!Xh || !Wq || !w_scale || !logits) return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
   if ((st = check_aligned(Xh, elem_bytes(dt), "Xh")) != HASTE_OK) return st;
   if ((st = check_aligned(Wq, 16, "Wq")) != HASTE_OK) return st;
@@ -1122,8 +1124,8 @@ haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtyp
   if (e == cudaSuccess) {
     ProfScope ps("head_forward_i8", s);
     const int ld = head8::pitch(d);
-    e = out_dt == HASTE_BF16 ? head8::launch_product<__nv_bfloat16>(B, H, ld, qx, sx, Wq, w_scale, logits, s)
-                             : head8::launch_product<float>(B, H, ld, qx, sx, Wq, w_scale, logits, s);
+    e = out_dt == HASTE_BF16 ? head8::launch_product<__nv_bfloat16>(B, H, ld, qx, sx, Wq, w_scale, logits, di.sms, s)
+                             : head8::launch_product<float>(B, H, ld, qx, sx, Wq, w_scale, logits, di.sms, s);
   }
   return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_head_forward_i8 launch");
 }

@@ -2,14 +2,13 @@
 //
 // Row quantisation (weights: one scale per label; features: one per sample):
 // s = max|x| / 127 rounded once to fp32, q = the exact quotient x / s rounded half
-// to even.  Product: z[b, h] = (sum_f qx[b, f] qw[h, f]) * (sx[b] * sw[h]), the sum
-// exact in 32 bits.
+// to even.  Product: z[b, h] = (float)(sum_f qx[b, f] qw[h, f]) * (sx[b] * sw[h]),
+// the sum exact in 32 bits (tcgen05 kind::i8).
 #include "common.cuh"
 
 namespace haste {
 namespace head8 {
 
-constexpr int kThreads = 256;
 constexpr int kMaxN = 131072;  // 127 * 127 * kMaxN < 2^31
 
 __host__ __device__ inline int pitch(int n) { return (n + 15) / 16 * 16; }
@@ -28,55 +27,391 @@ __device__ __forceinline__ int quantise(float x, float s) {
   return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// One CTA per row.  A row with a NaN or an infinity gets the scale NaN and zeros.
+// 8 consecutive elements of a row as fp32, 0 past its end; vec: the row starts on
+// a 16-byte boundary and holds whole vectors of 8.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_quantize_rows(const T* __restrict__ x, int n, int8_t* __restrict__ q,
-                                                            float* __restrict__ scale) {
-  __shared__ float red[kThreads / 32];
-  const int64_t r = blockIdx.x;
+__device__ __forceinline__ void load8(const T* __restrict__ row, int i, int n, bool vec, float (&v)[8]) {
+  if (vec && i + 8 <= n) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 r = *reinterpret_cast<const uint4*>(row + i);
+      const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(u[j] << 16);
+        v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      }
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(row + i), b = *reinterpret_cast<const float4*>(row + i + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < n ? Elem<T>::to_f(row[i + j]) : 0.f;
+  }
+}
+
+// One row per group of kWarps warps; every lane holds kKeep runs of 8 elements of
+// its row (rows of up to 256 kWarps kKeep elements are read once), longer rows are
+// read again from L2.  A row with a NaN or an infinity gets the scale NaN and zeros.
+constexpr int kQThreads = 256, kKeep = 4;
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict__ x, int64_t rows, int n, bool vec,
+                                                             int8_t* __restrict__ q, float* __restrict__ scale) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ float red[kQThreads / 32];
+  constexpr int kRowThreads = 32 * kWarps;
+  const int64_t r = (int64_t)blockIdx.x * (kQThreads / kRowThreads) + threadIdx.x / kRowThreads;
+  const int t = threadIdx.x % kRowThreads;
+  const bool live = r < rows;
   const int ld = pitch(n);
-  const T* xr = x + r * n;
+  const T* xr = x + (live ? r : 0) * n;
+  float keep[kKeep][8];
   float m = 0.f;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const float v = fabsf(Elem<T>::to_f(xr[i]));
-    m = v <= m ? m : v < INFINITY ? v : INFINITY;  // NaN counts as infinite
+  auto take = [&](const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(v[j]);
+      m = a <= m ? m : a < INFINITY ? a : INFINITY;  // NaN counts as infinite
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < kKeep; ++c) load8(xr, (c * kRowThreads + t) * 8, n, vec, keep[c]);
+#pragma unroll
+  for (int c = 0; c < kKeep; ++c) take(keep[c]);
+  for (int i = (kKeep * kRowThreads + t) * 8; i < n; i += kRowThreads * 8) {
+    float v[8];
+    load8(xr, i, n, vec, v);
+    take(v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-  for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, red[i]);
+  if constexpr (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, red[threadIdx.x / kRowThreads * kWarps + i]);
+  }
+  if (!live) return;
   const float s = m < INFINITY ? __fdiv_rn(m, 127.f) : NAN;
-  for (int i = threadIdx.x; i < ld; i += blockDim.x)
-    q[r * ld + i] = (int8_t)(i < n && s > 0.f ? quantise(Elem<T>::to_f(xr[i]), s) : 0);
-  if (threadIdx.x == 0) scale[r] = s;
-}
-
-// One thread per logit.
-template <typename O>
-__global__ void __launch_bounds__(128) k_head_i8(int H, int ld, const int8_t* __restrict__ qx,
-                                                 const float* __restrict__ sx, const int8_t* __restrict__ qw,
-                                                 const float* __restrict__ sw, O* __restrict__ out) {
-  const int64_t h = blockIdx.x * 128ll + threadIdx.x, b = blockIdx.y;
-  if (h >= H) return;
-  const int* x4 = reinterpret_cast<const int*>(qx + b * ld);
-  const int* w4 = reinterpret_cast<const int*>(qw + h * ld);
-  int acc = 0;
-  for (int i = 0; i < ld / 4; ++i) acc = __dp4a(x4[i], w4[i], acc);
-  out[b * H + h] = Elem<O>::from_f((float)acc * (sx[b] * sw[h]));
+  if (t == 0) scale[r] = s;
+  auto put = [&](int i, const float (&v)[8]) {
+    uint32_t w[2] = {0, 0};
+    if (s > 0.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j / 4] |= (uint32_t)(quantise(v[j], s) & 0xff) << (8 * (j % 4));
+    }
+    *reinterpret_cast<uint2*>(q + r * ld + i) = make_uint2(w[0], w[1]);
+  };
+#pragma unroll
+  for (int c = 0; c < kKeep; ++c) {
+    const int i = (c * kRowThreads + t) * 8;
+    if (i < ld) put(i, keep[c]);
+  }
+  for (int i = (kKeep * kRowThreads + t) * 8; i < ld; i += kRowThreads * 8) {
+    float v[8];
+    load8(xr, i, n, vec, v);
+    put(i, v);
+  }
 }
 
 template <typename T>
 cudaError_t launch_quantize(int64_t rows, int n, const void* x, int8_t* q, float* scale, cudaStream_t st) {
-  k_quantize_rows<T><<<(unsigned)rows, kThreads, 0, st>>>(static_cast<const T*>(x), n, q, scale);
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && n % 8 == 0;
+  const T* xp = static_cast<const T*>(x);
+  // a warp per row as long as its registers hold the row
+  if (n <= 256 * kKeep)
+    k_quantize_rows<T, 1><<<(unsigned)((rows + 7) / 8), kQThreads, 0, st>>>(xp, rows, n, vec, q, scale);
+  else
+    k_quantize_rows<T, 8><<<(unsigned)rows, kQThreads, 0, st>>>(xp, rows, n, vec, q, scale);
   return cudaGetLastError();
 }
 
+// ------------------------------------------------------------- the product
+// Persistent CTAs over tiles of 128 labels x BN samples.  The labels are the M
+// rows of the MMA (TMEM lanes), so that a warp's store of one sample covers 32
+// consecutive logits, and a batch of one still fills the instruction's M.
+//   warp 0     TMA producer: 128-byte runs of K of the weight and feature tiles
+//              into a ring of NS stages (128B swizzle)
+//   warp 1     MMA issuer: kind::i8, K = 32 per instruction, into one of two
+//              TMEM accumulators of BN columns
+//   warps 2-9  epilogue: warp (q, half) reads lane quarter q of its half of the
+//              columns, scales and stores
+constexpr int kThreads = 320;
+constexpr int kML = 128;      // labels per tile
+constexpr int kKB = 128;      // K bytes per stage
+constexpr int kMaxStages = 8;
+constexpr int kMaxBH = 1 << 30;  // B and H: tile coordinates are 32-bit
+// Tiles of the narrowest form a batch of B can take.
+inline int64_t max_tiles(int64_t B, int64_t H) { return (H + kML - 1) / kML * (B <= 64 ? 1 : (B + 63) / 64); }
+
+struct Args {
+  int B, H, nk;  // nk: K stages of a tile
+  int n_bt, n_tiles;
+  const float* sx;  // [B], readable up to a multiple of 256
+  const float* sw;
+  void* out;
+};
+
+template <int BN>
+constexpr int stages() {
+  constexpr int fit = 200 * 1024 / ((kML + BN) * kKB);
+  return fit < kMaxStages ? fit : kMaxStages;
+}
+template <int BN>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)stages<BN>() * (kML + BN) * kKB + 512;
+}
+
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Signed 8-bit operands, both K-major, 32-bit integer accumulator.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (!mbar_wait(bar, parity, g_wait_limit_ns)) {
+    *abort_flag = 1;
+    return false;
+  }
+  return true;
+}
+
+template <typename O, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_head_i8(Args a, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int NS = stages<BN>();
+  constexpr uint32_t kA = kML * kKB, kB = BN * kKB;
+  constexpr uint32_t kTmemCols = 2 * BN;
+  const uint32_t base = align1024(smem_u32(smem));
+  auto SA = [&](int st) -> uint32_t { return base + (uint32_t)st * (kA + kB); };
+  auto SB = [&](int st) -> uint32_t { return SA(st) + kA; };
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (base - smem_u32(smem)) + NS * (kA + kB));
+  uint64_t* full = bars;                 // [NS] tiles landed
+  uint64_t* empty = full + kMaxStages;   // [NS] tiles read (MMA commit)
+  uint64_t* acc_full = empty + kMaxStages;  // [2] accumulator complete
+  uint64_t* acc_empty = acc_full + 2;       // [2] accumulator read (8 epilogue warps)
+  uint64_t* done = acc_empty + 2;           // every MMA of the CTA finished
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 8);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (w == 1) {
+    tmem_alloc(tslot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  if (w == 0) {
+    if (lane == 0) {
+      // the weights do not depend on the quantisation kernel before this one: its
+      // end is awaited only before the first feature tile
+      bool waited = false;
+      int st = 0, ph = 0, issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < a.n_tiles && ok; t += gridDim.x) {
+        const int h0 = t / a.n_bt * kML, b0 = t % a.n_bt * BN;
+        for (int k = 0; k < a.nk; ++k) {
+          if (!wait_or_abort(&empty[st], ph ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ++issued;
+          mbar_arrive_expect_tx(&full[st], kA + kB);
+          tma_load_2d(SA(st), &tm_w, k * kKB, h0, &full[st]);
+          if (!waited) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
+          }
+          tma_load_2d(SB(st), &tm_x, k * kKB, b0, &full[st]);
+          if (++st == NS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // no copy may still be landing when the CTA exits
+      for (int j = issued > NS ? issued - NS : 0; j < issued; ++j) mbar_wait(&full[j % NS], (j / NS) & 1);
+    }
+  } else if (w == 1) {
+    constexpr uint32_t idesc = idesc_i8(kML, BN);
+    int st = 0, ph = 0, it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < a.n_tiles && ok; t += gridDim.x, ++it) {
+      const int ac = it & 1;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_empty[ac], ((it >> 1) & 1) ^ 1, abort_flag))) break;
+      tc_fence_after();
+      for (int k = 0; k < a.nk; ++k) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t ad = make_sdesc(SA(st), 16, 1024, kLayoutSw128), bd = make_sdesc(SB(st), 16, 1024, kLayoutSw128);
+#pragma unroll
+          for (int kk = 0; kk < kKB / 32; ++kk)
+            mma_i8(tmem + (uint32_t)(ac * BN), ad + 2 * kk, bd + 2 * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&empty[st]);
+          if (k + 1 == a.nk) mma_commit(&acc_full[ac]);
+        }
+        __syncwarp();
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (lane == 0) mma_commit(done);  // also after an abort: TMEM is freed only once the MMAs end
+    __syncwarp();
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kCols = BN / 2, CH = kCols < 16 ? kCols : 16;
+    const int q = w & 3, half = (w - 2) >> 2;
+    O* out = static_cast<O*>(a.out);
+    // bf16 logits of two neighbouring labels leave as one 4-byte store when every
+    // row starts on one (two 2-byte stores of a warp cover the same 64 bytes)
+    const bool pairs = sizeof(O) == 2 && (a.H & 1) == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
+    int it = 0;
+    for (int t = blockIdx.x; t < a.n_tiles; t += gridDim.x, ++it) {
+      const int ac = it & 1;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[ac], (it >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      const int h = t / a.n_bt * kML + q * 32 + lane, b0 = t % a.n_bt * BN + half * kCols;
+      const float sw = h < a.H ? a.sw[h] : 0.f;
+      const uint32_t src = tmem + (uint32_t)(ac * BN + half * kCols) + ((uint32_t)(q * 32) << 16);
+      for (int c = 0; c < kCols; c += CH) {
+        if (b0 + c >= a.B) break;
+        float v[CH];
+        if constexpr (CH == 16) tmem_ld16(src + (uint32_t)c, v);
+        else tmem_ld8(src + (uint32_t)c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < CH; i += 4) {
+          const float4 sx = *reinterpret_cast<const float4*>(a.sx + b0 + c + i);
+          v[i] = (float)__float_as_int(v[i]) * (sx.x * sw);
+          v[i + 1] = (float)__float_as_int(v[i + 1]) * (sx.y * sw);
+          v[i + 2] = (float)__float_as_int(v[i + 2]) * (sx.z * sw);
+          v[i + 3] = (float)__float_as_int(v[i + 3]) * (sx.w * sw);
+        }
+        O* row = out + (int64_t)(b0 + c) * a.H + h;
+        if (pairs) {
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int i = 0; i < CH; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+            // even lanes store this label and the next for column i, odd ones the
+            // previous label and this one for column i + 1
+            const uint32_t pk = odd ? pack_bf16x2(got, v[i + 1]) : pack_bf16x2(v[i], got);
+            const int col = i + (odd ? 1 : 0);
+            if (h < a.H && b0 + c + col < a.B)
+              *reinterpret_cast<uint32_t*>(row + (int64_t)col * a.H - (odd ? 1 : 0)) = pk;
+          }
+        } else if (h < a.H) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            if (b0 + c + i < a.B) row[(int64_t)i * a.H] = Elem<O>::from_f(v[i]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[ac]);
+    }
+    mbar_wait(done, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (w == 1) {
+    mbar_wait(done, 0);
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// 2D map of rows of ld bytes in boxes of 128 bytes x box_rows (128B swizzle), zeros
+// past the edges.
+inline cudaError_t tmap_i8(CUtensorMap* tm, const void* base, uint64_t ld, uint64_t rows, uint32_t box_rows) {
+  tail2::EncodeTiledFn enc = tail2::encode_tiled();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {ld, rows}, strides[1] = {ld};
+  const cuuint32_t box[2] = {kKB, box_rows}, estr[2] = {1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename O, int BN>
+cudaError_t launch_product_t(Args a, int ld, const int8_t* qx, const int8_t* qw, int sms, cudaStream_t st) {
+  a.n_bt = (a.B + BN - 1) / BN;
+  a.n_tiles = (a.H + kML - 1) / kML * a.n_bt;
+  CUtensorMap tm_w, tm_x;
+  cudaError_t e = tmap_i8(&tm_w, qw, ld, a.H, kML);
+  if (e == cudaSuccess) e = tmap_i8(&tm_x, qx, ld, a.B, BN);
+  auto kern = k_head_i8<O, BN>;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<BN>());
+  if (e != cudaSuccess) return e;
+  // the launch overlaps the quantisation kernel before it (griddepcontrol.wait)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.n_tiles < sms ? a.n_tiles : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<BN>();
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, tm_w, tm_x);
+}
+
+// Samples per tile: the whole batch if it fits one tile and the label tiles fill
+// the SMs; narrower tiles otherwise, down to 64.
 template <typename O>
 cudaError_t launch_product(int B, int H, int ld, const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,
-                           void* out, cudaStream_t st) {
-  k_head_i8<O><<<dim3((unsigned)((H + 127) / 128), B), 128, 0, st>>>(H, ld, qx, sx, qw, sw, static_cast<O*>(out));
-  return cudaGetLastError();
+                           void* out, int sms, cudaStream_t st) {
+  Args a{};
+  a.B = B;
+  a.H = H;
+  a.nk = (ld + kKB - 1) / kKB;
+  a.sx = sx;
+  a.sw = sw;
+  a.out = out;
+  const int64_t lt = (H + kML - 1) / kML;
+  int bn = B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : 256;
+  while (bn > 64 && lt * ((B + bn - 1) / bn) < sms) bn /= 2;
+  switch (bn) {
+    case 16: return launch_product_t<O, 16>(a, ld, qx, qw, sms, st);
+    case 32: return launch_product_t<O, 32>(a, ld, qx, qw, sms, st);
+    case 64: return launch_product_t<O, 64>(a, ld, qx, qw, sms, st);
+    case 128: return launch_product_t<O, 128>(a, ld, qx, qw, sms, st);
+    default: return launch_product_t<O, 256>(a, ld, qx, qw, sms, st);
+  }
 }
 
 }  // namespace head8

@@ -126,7 +126,8 @@ ARG, SHAPE, WS = H.HASTE_ERR_INVALID_ARG, H.HASTE_ERR_UNSUPPORTED_SHAPE, H.HASTE
     (_head, dict(dt=7), ARG), (_head, dict(odt=-1), ARG), (_head, dict(x=None), ARG), (_head, dict(w=None), ARG),
     (_head, dict(s=None), ARG), (_head, dict(out=None), ARG), (_head, dict(w=P + 4), ARG),
     (_head, dict(x=P + 1), ARG), (_head, dict(out=P + 2), ARG), (_head, dict(ws=None), ARG),
-    (_head, dict(ws=P + 8), ARG), (_head, dict(nws=511), WS),
+    (_head, dict(ws=P + 8), ARG), (_head, dict(nws=511), WS), (_head, dict(B=(1 << 30) + 1), SHAPE),
+    (_head, dict(B=1 << 26, Hh=1 << 30), SHAPE),
     (_logprob, dict(B=0), ARG), (_logprob, dict(N=0), ARG), (_logprob, dict(N=1 << 31), SHAPE),
     (_logprob, dict(dt=3), ARG), (_logprob, dict(z=None), ARG), (_logprob, dict(z=P + 2), ARG),
     (_logprob, dict(k=-1), ARG), (_logprob, dict(k=65), ARG), (_logprob, dict(N=1, k=2), ARG),
