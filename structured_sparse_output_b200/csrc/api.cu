@@ -1131,17 +1131,37 @@ haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtyp
 }
 
 // ---------------------------------------------------- softmax of the logits
+// 16-byte vectors of a row of logits; `logits` NULL: of rows that start anywhere.
+static int64_t logprob_vectors(const void* logits, int64_t N, haste_dtype_t dt) {
+  const bool on = logits && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+  return dt == HASTE_BF16 ? logprob::row_vectors<__nv_bfloat16>(N, on) : logprob::row_vectors<float>(N, on);
+}
+
 static haste_status_t check_logprob(int B, int64_t N, haste_dtype_t dt, const haste_targets_t& given, int64_t nnz) {
   if (dt != HASTE_F32 && dt != HASTE_BF16) return fail(HASTE_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
   if (B <= 0 || N <= 0) return fail(HASTE_ERR_INVALID_ARG, "B and N must be positive");
   if (N > 0x7fffffff) return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "N=%lld: label ids are 32-bit", (long long)N);
   if (nnz < 0 || nnz > 0x7fffffff) return fail(HASTE_ERR_INVALID_ARG, "nnz=%lld out of [0, 2^31)", (long long)nnz);
+  if (logprob::segments(logprob_vectors(nullptr, N, dt)) * B > 0x7fffffff)
+    return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "B=%d, N=%lld: more segments than a grid holds", B, (long long)N);
   if (nnz > 0 && !given.row_ptr) return fail(HASTE_ERR_INVALID_ARG, "given ids need their row_ptr");
   if (nnz > 0 && !given.ids) return fail(HASTE_ERR_INVALID_ARG, "ids is NULL");
   return HASTE_OK;
 }
 
-size_t haste_logprob_workspace_size(int32_t B, int64_t N, haste_dtype_t dt, int32_t k) { return 0; }
+// Workspace of haste_logprob: the partial sums and the rank keys of each segment of
+// rows that have several.
+static size_t logprob_ws(int B, int64_t N, haste_dtype_t dt, int k, size_t* keys) {
+  const int64_t n = logprob::segments(logprob_vectors(nullptr, N, dt));
+  *keys = n > 1 ? align256((size_t)B * n * 16) : 0;
+  return n > 1 ? *keys + align256((size_t)B * n * k * 8) : 0;
+}
+
+size_t haste_logprob_workspace_size(int32_t B, int64_t N, haste_dtype_t dt, int32_t k) {
+  if (B <= 0 || N <= 0 || N > 0x7fffffff || k < 0 || k > logprob::kMaxK) return 0;
+  size_t keys;
+  return logprob_ws(B, N, dt, k, &keys);
+}
 
 haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void* logits, haste_targets_t given,
                              int64_t nnz, int32_t k, float* logp, float* lse, float* entropy, float* top_logp,
@@ -1152,13 +1172,29 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void*
   if (!logits || (nnz > 0 && !logp) || (k > 0 && (!top_logp || !top_id)))
     return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
   if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
-  if ((st = check_ws(ws, ws_bytes, haste_logprob_workspace_size(B, N, dt, k))) != HASTE_OK) return st;
+  const int64_t vectors = logprob_vectors(logits, N, dt), n_seg = logprob::segments(vectors);
+  const int threads = logprob::seg_threads(vectors);
+  size_t keys;
+  if ((st = check_ws(ws, ws_bytes, logprob_ws(B, N, dt, k, &keys))) != HASTE_OK) return st;
+  if (n_seg > 1 && (st = check_aligned(ws, 16, "the workspace")) != HASTE_OK) return st;
   DeviceInfo di;
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  logprob::Args a{logits, N, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, k, logp, lse, entropy, top_logp, top_id};
-  ProfScope ps("logprob", s);
-  const cudaError_t e = dt == HASTE_BF16 ? logprob::launch<__nv_bfloat16>(B, a, s) : logprob::launch<float>(B, a, s);
+  logprob::Args a{logits, N,       nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, k, (int)n_seg, logp, lse,
+                  entropy, top_logp, top_id};
+  if (n_seg > 1) {
+    a.part = static_cast<float4*>(ws);
+    a.keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(ws) + keys);
+  }
+  cudaError_t e;
+  {
+    ProfScope ps("logprob", s);
+    e = dt == HASTE_BF16 ? logprob::launch<__nv_bfloat16>(B, threads, a, s) : logprob::launch<float>(B, threads, a, s);
+  }
+  if (e == cudaSuccess && n_seg > 1) {
+    ProfScope ps("logprob_join", s);
+    e = dt == HASTE_BF16 ? logprob::launch_join<__nv_bfloat16>(B, a, s) : logprob::launch_join<float>(B, a, s);
+  }
   return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_logprob launch");
 }
 
@@ -1178,11 +1214,13 @@ haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dt, co
   DeviceInfo di;
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  logprob::GradArgs a{logits, N, lse, entropy, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, d_logp, d_entropy,
+  const int64_t vectors = logprob_vectors(logits, N, dt);
+  const int threads = logprob::seg_threads(vectors);
+  logprob::GradArgs a{logits, N, (int)logprob::segments(vectors), lse, entropy, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, d_logp, d_entropy,
                       d_logits};
   ProfScope ps("logprob_backward", s);
   const cudaError_t e =
-      dt == HASTE_BF16 ? logprob::launch_grad<__nv_bfloat16>(B, a, s) : logprob::launch_grad<float>(B, a, s);
+      dt == HASTE_BF16 ? logprob::launch_grad<__nv_bfloat16>(B, threads, a, s) : logprob::launch_grad<float>(B, threads, a, s);
   return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_logprob_backward launch");
 }
 

@@ -123,7 +123,7 @@ def _tptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
     return int(stream) if not hasattr(stream, "cuda_stream") else stream.cuda_stream
 
 
@@ -416,13 +416,30 @@ def haste_head_backward(Xh, Wh, dYh, dWh, dXh, ws, stream=None) -> None:
                                      _tptr(dXh), p, n, _stream(stream)), "haste_head_backward")
 
 
-def _current_device(**tensors):
-    """Every tensor on the current CUDA device: the calls below launch there."""
+def _device_of(t, name: str) -> int:
+    """The tensor's device, which must be the current one: the calls below launch there."""
     import torch
-    _same_device(None, **tensors)
-    dev = next(t.device for t in tensors.values() if t is not None)
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, but cuda:{torch.cuda.current_device()} is current")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}; tensors must be CUDA tensors (the library reads them on the GPU)")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
+    return dev
+
+
+def _ptr_on(t, name: str, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor on device `dev` (None stays None)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}; the call's tensors must be CUDA tensors on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ws_on(ws, dev: int):
+    return (_ptr_on(ws, "ws", dev), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
 
 
 # ------------------------------------------------------- dense head in 8 bits
@@ -437,11 +454,11 @@ def haste_quantize_rows(x, q, scale, stream=None) -> None:
     import torch
     rows, n = x.shape
     code = dtype_code(x)
-    _expect(q, "q", (rows, haste_i8_pitch(n)), torch.int8)
+    _expect(q, "q", (rows, (n + 15) // 16 * 16), torch.int8)
     _expect(scale, "scale", (rows,), torch.float32)
-    _current_device(x=x, q=q, scale=scale)
-    _check(lib().haste_quantize_rows(rows, n, code, _tptr(x), _tptr(q), _tptr(scale), _stream(stream)),
-           "haste_quantize_rows")
+    dev = _device_of(x, "x")
+    _check(lib().haste_quantize_rows(rows, n, code, _ptr_on(x, "x", dev), _ptr_on(q, "q", dev),
+                                     _ptr_on(scale, "scale", dev), _stream(stream)), "haste_quantize_rows")
 
 
 def haste_head_i8_workspace_size(B: int, H: int, d: int) -> int:
@@ -455,12 +472,13 @@ def haste_head_forward_i8(Xh, Wq, w_scale, logits, ws, stream=None) -> None:
     B, d = Xh.shape
     H = Wq.shape[0]
     code, out_code = dtype_code(Xh), dtype_code(logits)
-    _expect(Wq, "Wq", (H, haste_i8_pitch(d)), torch.int8)
+    _expect(Wq, "Wq", (H, (d + 15) // 16 * 16), torch.int8)
     _expect(w_scale, "w_scale", (H,), torch.float32)
     _expect(logits, "logits", (B, H))
-    _current_device(Xh=Xh, Wq=Wq, w_scale=w_scale, logits=logits, ws=ws)
-    p, n = _ws(ws)
-    _check(lib().haste_head_forward_i8(B, H, d, code, _tptr(Xh), _tptr(Wq), _tptr(w_scale), out_code, _tptr(logits),
+    dev = _device_of(Xh, "Xh")
+    p, n = _ws_on(ws, dev)
+    _check(lib().haste_head_forward_i8(B, H, d, code, _ptr_on(Xh, "Xh", dev), _ptr_on(Wq, "Wq", dev),
+                                       _ptr_on(w_scale, "w_scale", dev), out_code, _ptr_on(logits, "logits", dev),
                                        p, n, _stream(stream)), "haste_head_forward_i8")
 
 
@@ -500,12 +518,13 @@ def haste_logprob(logits, row_ptr=None, ids=None, logp=None, lse=None, entropy=N
         k = top_id.shape[-1]
         _expect(top_id, "top_id", (B, k), torch.int32)
         _expect(top_logp, "top_logp", (B, k), torch.float32)
-    _current_device(logits=logits, row_ptr=row_ptr, ids=ids, logp=logp, lse=lse, entropy=entropy, top_logp=top_logp,
-                    top_id=top_id, ws=ws)
-    p, n = _ws(ws)
-    _check(lib().haste_logprob(B, N, code, _tptr(logits), Targets(_tptr(row_ptr), _tptr(ids)), nnz, k, _tptr(logp),
-                               _tptr(lse), _tptr(entropy), _tptr(top_logp), _tptr(top_id), p, n, _stream(stream)),
-           "haste_logprob")
+    dev = _device_of(logits, "logits")
+    p, n = _ws_on(ws, dev)
+    given = Targets(_ptr_on(row_ptr, "row_ptr", dev), _ptr_on(ids, "ids", dev))
+    _check(lib().haste_logprob(B, N, code, _ptr_on(logits, "logits", dev), given, nnz, k, _ptr_on(logp, "logp", dev),
+                               _ptr_on(lse, "lse", dev), _ptr_on(entropy, "entropy", dev),
+                               _ptr_on(top_logp, "top_logp", dev), _ptr_on(top_id, "top_id", dev), p, n,
+                               _stream(stream)), "haste_logprob")
 
 
 def haste_logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy, d_logits, stream=None) -> None:
@@ -521,8 +540,9 @@ def haste_logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy
         if t is not None or (n == "entropy" and d_entropy is not None):
             _expect(t, n, (B,), torch.float32)
     _expect(d_logits, "d_logits", (B, N), logits.dtype)
-    _current_device(logits=logits, lse=lse, entropy=entropy, row_ptr=row_ptr, ids=ids, d_logp=d_logp,
-                    d_entropy=d_entropy, d_logits=d_logits)
-    _check(lib().haste_logprob_backward(B, N, code, _tptr(logits), _tptr(lse), _tptr(entropy),
-                                        Targets(_tptr(row_ptr), _tptr(ids)), nnz, _tptr(d_logp), _tptr(d_entropy),
-                                        _tptr(d_logits), _stream(stream)), "haste_logprob_backward")
+    dev = _device_of(logits, "logits")
+    given = Targets(_ptr_on(row_ptr, "row_ptr", dev), _ptr_on(ids, "ids", dev))
+    _check(lib().haste_logprob_backward(B, N, code, _ptr_on(logits, "logits", dev), _ptr_on(lse, "lse", dev),
+                                        _ptr_on(entropy, "entropy", dev), given, nnz, _ptr_on(d_logp, "d_logp", dev),
+                                        _ptr_on(d_entropy, "d_entropy", dev), _ptr_on(d_logits, "d_logits", dev),
+                                        _stream(stream)), "haste_logprob_backward")
