@@ -1131,10 +1131,8 @@ haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtyp
 }
 
 // ---------------------------------------------------- softmax of the logits
-// 16-byte vectors of a row of logits; `logits` NULL: of rows that start anywhere.
-static int64_t logprob_vectors(const void* logits, int64_t N, haste_dtype_t dt) {
-  const bool on = logits && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
-  return dt == HASTE_BF16 ? logprob::row_vectors<__nv_bfloat16>(N, on) : logprob::row_vectors<float>(N, on);
+static int64_t logprob_blocks(int64_t N, haste_dtype_t dt) {
+  return dt == HASTE_BF16 ? logprob::row_blocks<__nv_bfloat16>(N) : logprob::row_blocks<float>(N);
 }
 
 static haste_status_t check_logprob(int B, int64_t N, haste_dtype_t dt, const haste_targets_t& given, int64_t nnz) {
@@ -1142,17 +1140,15 @@ static haste_status_t check_logprob(int B, int64_t N, haste_dtype_t dt, const ha
   if (B <= 0 || N <= 0) return fail(HASTE_ERR_INVALID_ARG, "B and N must be positive");
   if (N > 0x7fffffff) return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "N=%lld: label ids are 32-bit", (long long)N);
   if (nnz < 0 || nnz > 0x7fffffff) return fail(HASTE_ERR_INVALID_ARG, "nnz=%lld out of [0, 2^31)", (long long)nnz);
-  if (logprob::segments(logprob_vectors(nullptr, N, dt)) * B > 0x7fffffff)
-    return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "B=%d, N=%lld: more segments than a grid holds", B, (long long)N);
   if (nnz > 0 && !given.row_ptr) return fail(HASTE_ERR_INVALID_ARG, "given ids need their row_ptr");
   if (nnz > 0 && !given.ids) return fail(HASTE_ERR_INVALID_ARG, "ids is NULL");
   return HASTE_OK;
 }
 
-// Workspace of haste_logprob: the partial sums and the rank keys of each segment of
-// rows that have several.
+// Workspace of haste_logprob: the sums and the rank keys of each run of rows that
+// are split.
 static size_t logprob_ws(int B, int64_t N, haste_dtype_t dt, int k, size_t* keys) {
-  const int64_t n = logprob::segments(logprob_vectors(nullptr, N, dt));
+  const int64_t n = logprob::runs(B, logprob_blocks(N, dt), logprob::kCtas);
   *keys = n > 1 ? align256((size_t)B * n * 16) : 0;
   return n > 1 ? *keys + align256((size_t)B * n * k * 8) : 0;
 }
@@ -1172,26 +1168,25 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void*
   if (!logits || (nnz > 0 && !logp) || (k > 0 && (!top_logp || !top_id)))
     return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
   if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
-  const int64_t vectors = logprob_vectors(logits, N, dt), n_seg = logprob::segments(vectors);
-  const int threads = logprob::seg_threads(vectors);
+  const int n_run = (int)logprob::runs(B, logprob_blocks(N, dt), logprob::kCtas);
   size_t keys;
   if ((st = check_ws(ws, ws_bytes, logprob_ws(B, N, dt, k, &keys))) != HASTE_OK) return st;
-  if (n_seg > 1 && (st = check_aligned(ws, 16, "the workspace")) != HASTE_OK) return st;
+  if (n_run > 1 && (st = check_aligned(ws, 16, "the workspace")) != HASTE_OK) return st;
   DeviceInfo di;
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  logprob::Args a{logits, N,       nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, k, (int)n_seg, logp, lse,
+  logprob::Args a{logits, N,       nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, k, n_run, logp, lse,
                   entropy, top_logp, top_id};
-  if (n_seg > 1) {
+  if (n_run > 1) {
     a.part = static_cast<float4*>(ws);
     a.keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(ws) + keys);
   }
   cudaError_t e;
   {
     ProfScope ps("logprob", s);
-    e = dt == HASTE_BF16 ? logprob::launch<__nv_bfloat16>(B, threads, a, s) : logprob::launch<float>(B, threads, a, s);
+    e = dt == HASTE_BF16 ? logprob::launch<__nv_bfloat16>(B, a, s) : logprob::launch<float>(B, a, s);
   }
-  if (e == cudaSuccess && n_seg > 1) {
+  if (e == cudaSuccess && n_run > 1) {
     ProfScope ps("logprob_join", s);
     e = dt == HASTE_BF16 ? logprob::launch_join<__nv_bfloat16>(B, a, s) : logprob::launch_join<float>(B, a, s);
   }
@@ -1214,13 +1209,12 @@ haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dt, co
   DeviceInfo di;
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t vectors = logprob_vectors(logits, N, dt);
-  const int threads = logprob::seg_threads(vectors);
-  logprob::GradArgs a{logits, N, (int)logprob::segments(vectors), lse, entropy, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, d_logp, d_entropy,
+  const int n_run = (int)logprob::runs(B, logprob_blocks(N, dt), logprob::kGradCtas);
+  logprob::GradArgs a{logits, N, n_run, lse, entropy, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, d_logp, d_entropy,
                       d_logits};
   ProfScope ps("logprob_backward", s);
   const cudaError_t e =
-      dt == HASTE_BF16 ? logprob::launch_grad<__nv_bfloat16>(B, threads, a, s) : logprob::launch_grad<float>(B, threads, a, s);
+      dt == HASTE_BF16 ? logprob::launch_grad<__nv_bfloat16>(B, a, s) : logprob::launch_grad<float>(B, a, s);
   return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_logprob_backward launch");
 }
 

@@ -7,6 +7,8 @@
 // join by rescaling S and T to the common maximum.
 // Rank order of the alternatives: larger logit first, equal logits by smaller id.
 // Gradient: dz_j = sum_{i: id_i = j} g_i - p_j (sum_i g_i + gH (log p_j + entropy)).
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace haste {
@@ -14,8 +16,11 @@ namespace logprob {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxK = 64;
-constexpr int kV = 4;        // 16-byte vectors per thread: a segment of 64 bytes a thread, held in registers
-constexpr int kGroups = 128;  // groups of threads whose maxima bound the k-th best logit
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kV = 4;                     // 16-byte vectors of a thread in a block of a row
+constexpr int kBlock = kThreads * kV;     // vectors of a block: 16 KB of a row
+constexpr int kCap = 256;                 // competing logits that a warp keeps
+constexpr int kMaxRuns = 1024;            // runs of a row
 
 struct Args {
   const void* logits;  // [B, N]
@@ -24,20 +29,20 @@ struct Args {
   const int32_t* ids;
   int64_t nnz;
   int k;
-  int n_seg;  // segments of a row
+  int n_run;  // runs that a row is split into, one CTA each
   float* logp;
   float* lse;
   float* entropy;
   float* top_logp;
   int32_t* top_id;
-  float4* part;    // [B, n_seg] (m, S, T): partial sums when n_seg > 1
-  uint64_t* keys;  // [B, n_seg, k] rank keys of the segment's best, descending, 0 = none
+  float4* part;    // [B, n_run] (m, S, T): the runs' sums when n_run > 1
+  uint64_t* keys;  // [B, n_run, k] rank keys of the run's best, descending, 0 = none
 };
 
 struct GradArgs {
   const void* logits;
   int64_t N;
-  int n_seg;
+  int n_run;
   const float* lse;
   const float* entropy;
   const int32_t* row_ptr;
@@ -50,15 +55,18 @@ struct GradArgs {
 
 // A whole number that orders (z, id) as the alternatives are ranked: larger z
 // first (-0 as 0, NaN as -inf), then smaller id.  0 is below every pair.
-__device__ __forceinline__ uint64_t rank_key(float z, uint32_t id) {
+__device__ __forceinline__ uint32_t rank_value(float z) {
   z = z == z ? z + 0.f : -INFINITY;
   const uint32_t u = __float_as_uint(z);
-  const uint32_t o = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-  return ((uint64_t)o << 32) | (uint32_t)~id;
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t rank_key(float z, uint32_t id) {
+  return ((uint64_t)rank_value(z) << 32) | (uint32_t)~id;
 }
 __device__ __forceinline__ uint32_t key_id(uint64_t key) { return ~(uint32_t)key; }
-__device__ __forceinline__ float key_value(uint64_t key) {
+__device__ __forceinline__ float key_value(uint64_t key) {  // -inf for what is below every pair
   const uint32_t o = (uint32_t)(key >> 32);
+  if (o < 0x007fffffu) return -INFINITY;
   return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
 
@@ -92,16 +100,17 @@ template <typename T>
 struct Row {
   static constexpr int kE = 16 / sizeof(T);  // elements of a vector
   const T* z;
-  int64_t N;
+  uint32_t N;
   int head;  // elements of the first vector before the row
-  __device__ Row(const void* base, int64_t b, int64_t n) : z(static_cast<const T*>(base) + b * n), N(n) {
+  __device__ Row(const void* base, int64_t b, int64_t n) : z(static_cast<const T*>(base) + b * n), N((uint32_t)n) {
     head = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
   }
   // column of the first element of vector v (negative in the first vector of a row off the boundary)
-  __device__ int64_t column(int64_t v) const { return v * kE - head; }
-  __device__ uint4 load(int64_t v) const {
+  __device__ int64_t column(uint32_t v) const { return (int64_t)v * kE - head; }
+  __device__ bool whole(int64_t j) const { return j >= 0 && j + kE <= (int64_t)N; }
+  __device__ uint4 load(uint32_t v) const {
     const int64_t j = column(v);
-    if (j >= 0 && j + kE <= N) return *reinterpret_cast<const uint4*>(z + j);
+    if (whole(j)) return *reinterpret_cast<const uint4*>(z + j);
     constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
     uint32_t u[4] = {kNone, kNone, kNone, kNone};
     if (j < N)
@@ -138,31 +147,52 @@ inline int64_t row_vectors(int64_t N, bool on_boundary) {
   return N % kE == 0 ? N / kE + (on_boundary ? 0 : 1) : (N + kE - 2) / kE + 1;
 }
 
-// The largest tau such that at least k of the block's keys are >= tau, and exactly
-// k when the keys are distinct; key[i] = 0 does not count.  At least k must exist.
+// The k-th largest of the block's keys (kN per thread, distinct but for 0, which
+// does not count; at least k of them), or a lower bound that k keys reach and no
+// other: digits of 8 bits from the top, each by a histogram of the keys that share
+// the digits before.
 template <int kN>
-__device__ __forceinline__ uint64_t kth_key(const uint64_t (&key)[kN], int k) {
-  uint64_t tau = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const uint64_t c = tau | (1ull << bit);
-    int n = 0;
-    if constexpr (kN == 1) {
-      n = __syncthreads_count(key[0] >= c);
-    } else {
+__device__ uint64_t kth_key(const uint64_t (&key)[kN], int k, int* hist, int* found) {
+  uint64_t prefix = 0, mask = 0;
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (key[i] != 0 && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & 255], 1);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // lane l: bins 8 (31 - l) .. + 7, so that a prefix sum counts from the top
+      const int* bin = hist + 8 * (31 - threadIdx.x);
       int mine = 0;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) mine += key[i] >= c;
-      // counts of up to kN per thread: one vote per bit of the count
+      for (int i = 0; i < 8; ++i) mine += bin[i];
+      int upto = mine;
 #pragma unroll
-      for (int s = 0; (1 << s) <= kN; ++s) n += __syncthreads_count((mine >> s) & 1) << s;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if ((int)threadIdx.x >= o) upto += v;
+      }
+      int above = upto - mine;
+      if (above < k && upto >= k) {
+        int i = 7;
+        while (above + bin[i] < k) above += bin[i--];
+        found[0] = 8 * (31 - threadIdx.x) + i;
+        found[1] = k - above;
+        found[2] = bin[i] == k - above;
+      }
     }
-    if (n >= k) tau = c;
-    if (n == k) break;
+    __syncthreads();
+    prefix |= (uint64_t)found[0] << shift;
+    mask |= (uint64_t)255 << shift;
+    k = found[1];
+    if (found[2]) break;
   }
-  return tau;
+  return prefix;
 }
 
-// What a row needs besides its sums, from m, S and T of the whole row.
+// What a row needs besides its sums, from m, S and T of the whole row (S = 0 only
+// where every logit is -inf: the largest contributes 1).
 struct RowStats {
   float m, log_s;
   bool none;
@@ -171,8 +201,8 @@ struct RowStats {
 __device__ __forceinline__ RowStats row_stats(float m, float S) {
   RowStats r;
   r.m = m;
-  r.none = m == -INFINITY;
-  r.log_s = m < INFINITY ? logf(S) : NAN;  // a NaN or +inf in the row
+  r.none = S == 0.f;
+  r.log_s = logf(S);  // NaN for a NaN or +inf in the row
   return r;
 }
 template <typename T>
@@ -189,187 +219,361 @@ __device__ __forceinline__ void write_row(const Args& a, int64_t b, const T* z, 
   }
 }
 
-// One CTA per segment of a row.  The segment stays in registers: its maximum, then
-// its sums and its k best.  The k-th largest of the maxima of 128 groups of threads
-// is a lower bound of the k-th best logit, so only the few logits at or above it
-// compete; where too many do (long runs of equal logits), or a NaN hides a maximum,
-// the k-th best thread maximum decides, above which lie at most k threads' logits.
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8) k_logprob(Args a) {
-  constexpr int kE = 16 / sizeof(T), kWarps = kThreads / 32, kLanes = kThreads / kGroups;
-  constexpr int kCand = kMaxK * kV * kE;  // the logits of k threads
-  __shared__ float warp_m[kWarps], warp_s[kWarps], warp_t[kWarps];
-  __shared__ __align__(16) float group_m[kGroups];
-  __shared__ float tau_s;
-  __shared__ int n_cand;
-  __shared__ uint64_t cand[kCand];
-  const int64_t b = blockIdx.x / a.n_seg;
-  const int seg = blockIdx.x % a.n_seg, t = threadIdx.x;
+// Competing logits of one warp: the keys at or above `tau`, of which fewer than k
+// can be beaten by the others.
+struct Keep {
+  int n;
+  uint64_t tau;
+};
+
+// Raise tau until at most kCap / 2 of the warp's keys reach it, and still k do.
+__device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
+  const int lane = threadIdx.x & 31;
+  uint64_t key[kCap / 32];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kCap / 32; ++i) key[i] = i * 32 + lane < s.n ? buf[i * 32 + lane] : 0;
+  uint64_t c = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t up = c | (1ull << bit);
+    int cnt = 0;
+#pragma unroll
+    for (int i = 0; i < kCap / 32; ++i) cnt += __popc(__ballot_sync(0xffffffffu, key[i] >= up));
+    if (cnt >= k) c = up;
+    if (cnt >= k && cnt <= kCap / 2) break;
+  }
+  int at = 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kCap / 32; ++i) {
+    const bool in = key[i] >= c && key[i] != 0;
+    const uint32_t who = __ballot_sync(0xffffffffu, in);
+    if (in) buf[at + __popc(who & ((1u << lane) - 1))] = key[i];
+    at += __popc(who);
+  }
+  __syncwarp();
+  return Keep{at, c > s.tau ? c : s.tau};
+}
+
+// Add the logits of one vector of every lane that reach tau; hit: bits of the
+// lane's elements whose value does (or all of them, where tau's value is -inf).
+template <typename T>
+__device__ __forceinline__ Keep take(uint64_t* buf, Keep s, const uint4& raw, uint32_t hit, int64_t j, uint32_t N,
+                                     int k) {
+  const int lane = threadIdx.x & 31;
+  while (__any_sync(0xffffffffu, hit != 0)) {
+    uint64_t key = 0;
+    if (hit) {
+      const int e = __ffs(hit) - 1, wi = sizeof(T) == 2 ? e >> 1 : e;
+      hit &= hit - 1;
+      uint32_t u = wi == 0 ? raw.x : wi == 1 ? raw.y : wi == 2 ? raw.z : raw.w;
+      if (sizeof(T) == 2) u = (e & 1) ? u & 0xffff0000u : u << 16;
+      const int64_t col = j + e;
+      if (col >= 0 && col < (int64_t)N) key = rank_key(__uint_as_float(u), (uint32_t)col);
+    }
+    uint32_t who = __ballot_sync(0xffffffffu, key >= s.tau);
+    if (s.n + __popc(who) > kCap) {
+      s = shrink(buf, s, k);
+      who = __ballot_sync(0xffffffffu, key >= s.tau);
+    }
+    if (key >= s.tau) buf[s.n + __popc(who & ((1u << lane) - 1))] = key;
+    s.n += __popc(who);
+  }
+  return s;
+}
+
+// A lower bound of the k-th best of what the block's threads have seen, from their
+// maxima: the k-th largest of the maxima of kG groups of threads (k <= kG), as a
+// rank value without its low 7 bits, which tell equal maxima apart.
+template <int kG>
+__device__ uint32_t bound_of(float mx, int k, uint32_t* group, uint32_t* out) {
+  constexpr int kL = kThreads / kG, kPart = kG / kL;  // lanes of a group, groups that a lane compares with
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int o = 1; o < kL; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const uint32_t mine = (rank_value(mx) & ~127u) | (uint32_t)(t / kL);
+  if (t % kL == 0) group[t / kL] = mine;
+  __syncthreads();
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < kPart; i += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(&group[t % kL * kPart + i]);
+    above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+  }
+#pragma unroll
+  for (int o = 1; o < kL; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+  if (above == k - 1 && t % kL == 0) *out = mine & ~127u;
+  __syncthreads();
+  return *out;
+}
+
+// The k largest of the keys that the block's threads hold (kN each, distinct but
+// for 0, at least min(k, their number) wanted): emit(rank, key), by any thread.
+template <int kN, typename Emit>
+__device__ void emit_best(const uint64_t (&key)[kN], int k, int* hist, int* found, uint64_t* best, int* n_best,
+                          Emit emit) {
+  const uint64_t tau = kth_key(key, k, hist, found);
+  if (threadIdx.x == 0) *n_best = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    if (key[i] != 0 && key[i] >= tau) best[atomicAdd(n_best, 1)] = key[i];
+  __syncthreads();
+  if ((int)threadIdx.x < k) {
+    const uint64_t mine = best[threadIdx.x];
+    int rank = 0;
+    for (int i = 0; i < k; ++i) rank += best[i] > mine;
+    emit(rank, mine);
+  }
+}
+
+// Sums of one thread, warp or block around a reference mu (finite): S = sum
+// e^(z - mu), T = sum e^(z - mu) (mu - z).
+struct Sums {
+  float mu, S, T;
+  __device__ void move(float to) {  // to >= mu
+    const float d = fmaxf(mu - to, -200.f), w = ex2(d * kLog2e);
+    T = w * fmaf(-S, d, T);
+    S *= w;
+    mu = to;
+  }
+};
+
+// -inf counts as `lo`, whose e^(lo - mu) is 0 in fp32: the sums then meet no
+// infinity times 0.  A multiple of mu goes into the distance so that lo differs from
+// mu in bf16, too.
+__device__ __forceinline__ float floor_of(float mu) { return mu - fmaxf(200.f, 0.02f * fabsf(mu)); }
+constexpr float kDeep = -3.2e38f;  // no such floor exists below it
+
+// The sums of one vector.  Logits are raised to the floor before they are widened:
+// two at a time in bf16 (max keeps a NaN).
+template <typename T, bool kIsDeep>
+__device__ __forceinline__ void sum_vector(Sums& s, const uint4& raw, float lo) {
+  constexpr int kE = 16 / sizeof(T);
+  float v[kE];
+  if constexpr (sizeof(T) == 2 && !kIsDeep) {
+    const __nv_bfloat162 lo2 = __float2bfloat162_rn(lo);
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&u[i]), lo2);
+      c[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    unpack<T>(make_uint4(c[0], c[1], c[2], c[3]), v);
+  } else {
+    unpack<T>(raw, v);
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+      if (!kIsDeep) v[e] = max_nan(v[e], lo);
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    float d = v[e] - s.mu;
+    if (kIsDeep) d = max_nan(d, -200.f);
+    const float x = ex2(d * kLog2e);
+    s.S += x;
+    s.T = fmaf(-x, d, s.T);
+  }
+}
+
+// One CTA per run of a row: blocks of 256 threads x 64 bytes, the next block's
+// loads in flight while one is summed.  The threads' maxima bound the k-th best
+// logit from below, over the first block and again after 2, 4, 8 .. blocks; a warp
+// looks at single logits only where a vector's maximum reaches the bound.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) k_logprob(Args a) {
+  constexpr int kE = 16 / sizeof(T);
+  __shared__ float red[3][kWarps];
+  __shared__ __align__(16) uint32_t group[128];
+  __shared__ uint32_t tau_s;
+  __shared__ int n_keep[kWarps], hist[256], found[3], n_best;
+  __shared__ uint64_t keep_buf[kWarps][kCap], flat[kCap];
+  __shared__ uint64_t best[kMaxK];
+  const int64_t b = blockIdx.x / a.n_run;
+  const int run = blockIdx.x % a.n_run, t = threadIdx.x, w = t >> 5, lane = t & 31;
   const Row<T> row(a.logits, b, a.N);
-  const int64_t v0 = (int64_t)seg * (kThreads * kV) + t;
+  const int n_blocks = (int)((a.N + row.head + kE * (int64_t)kBlock - 1) / (kE * (int64_t)kBlock));
+  const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
 
   uint4 raw[kV];
+  uint32_t v0 = (uint32_t)blk0 * kBlock + t;
 #pragma unroll
   for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
-  if (t == 0) n_cand = 0;
-  float mine = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kV; ++i) {
+  auto vector_max = [](const uint4& r) {  // NaN is ignored here; it ends up in S
     float v[kE];
-    unpack<T>(raw[i], v);
+    unpack<T>(r, v);
+    float m = v[0];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) mine = max_nan(mine, v[e]);
+    for (int e = 1; e < kE; ++e) m = fmaxf(m, v[e]);
+    return m;
+  };
+  float mx = -INFINITY;  // of what this thread has seen
+#pragma unroll
+  for (int i = 0; i < kV; ++i) mx = fmaxf(mx, vector_max(raw[i]));
+  auto bound = [&] { return a.k <= 16 ? bound_of<64>(mx, a.k, group, &tau_s) : bound_of<128>(mx, a.k, group, &tau_s); };
+  float m = mx;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[0][w] = m;
+  Keep keep{0, ~0ull};
+  float tau_f = INFINITY;
+  if (a.k > 0) {
+    keep.tau = (uint64_t)bound() << 32;
+    tau_f = key_value(keep.tau);
+  } else {
+    __syncthreads();
   }
-  float g = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    if (o == kLanes && t % kLanes == 0) group_m[t / kLanes] = g;
-    g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
-  }
-  if ((t & 31) == 0) warp_m[t >> 5] = g;
-  __syncthreads();
-  float m = warp_m[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) m = max_nan(m, warp_m[i]);
+  for (int i = 0; i < kWarps; ++i) m = fmaxf(m, red[0][i]);
+  Sums s{m < INFINITY ? fmaxf(m, -FLT_MAX) : 0.f, 0.f, 0.f};
+  float lo = floor_of(s.mu);
+  bool inf = !(m < INFINITY);
 
-  // the k-th largest group maximum
-  if (a.k > 0 && t < kGroups) {
-    const float v = group_m[t];
-    int rank = 0;
-#pragma unroll 8
-    for (int i = 0; i < kGroups; i += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&group_m[i]);
-      rank += (o.x > v || (o.x == v && i < t)) + (o.y > v || (o.y == v && i + 1 < t)) +
-              (o.z > v || (o.z == v && i + 2 < t)) + (o.w > v || (o.w == v && i + 3 < t));
+  for (int blk = blk0; blk < blk1; ++blk) {
+    uint4 cur[kV];
+    const uint32_t v_cur = v0;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) cur[i] = raw[i];
+    v0 += kBlock;
+    if (blk + 1 < blk1) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
     }
-    if (rank == a.k - 1) tau_s = v;
-  }
-  float S = 0.f, Tt = 0.f;
+    const int seen = blk - blk0;
+    if (a.k > 0 && seen >= 2 && (seen & (seen - 1)) == 0) {
+      const uint64_t up = (uint64_t)bound() << 32;
+      if (up > keep.tau) {
+        keep.tau = up;
+        tau_f = key_value(up);
+      }
+    }
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    float v[kE];
-    unpack<T>(raw[i], v);
+    for (int i = 0; i < kV; ++i) {
+      const float vm = vector_max(cur[i]);
+      mx = fmaxf(mx, vm);
+      if (vm > s.mu) {
+        if (vm < INFINITY) s.move(vm);
+        else inf = true;
+        lo = floor_of(s.mu);
+      }
+      if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0) {
+        float v[kE];
+        unpack<T>(cur[i], v);
+        uint32_t hit = 0;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const float d = fmaxf(v[e] - m, -200.f), x = ex2(d * kLog2e);  // -inf: e^-200 is 0 in fp32
-      S += x;
-      Tt = fmaf(-x, d, Tt);
+        for (int e = 0; e < kE; ++e) hit |= (v[e] >= tau_f || tau_f == -INFINITY) ? 1u << e : 0u;
+        keep = take<T>(keep_buf[w], keep, cur[i], hit, row.column(v_cur + i * kThreads), row.N, a.k);
+        tau_f = key_value(keep.tau);
+      }
+      if (s.mu > kDeep) sum_vector<T, false>(s, cur[i], lo);
+      else sum_vector<T, true>(s, cur[i], lo);
     }
   }
+
+  // join the threads' sums around the run's maximum
+  float mu = s.mu;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    S += __shfl_xor_sync(0xffffffffu, S, o);
-    Tt += __shfl_xor_sync(0xffffffffu, Tt, o);
-  }
-  if ((t & 31) == 0) {
-    warp_s[t >> 5] = S;
-    warp_t[t >> 5] = Tt;
+  for (int o = 16; o > 0; o >>= 1) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+  inf = __any_sync(0xffffffffu, inf);
+  __syncthreads();
+  if (lane == 0) {
+    red[0][w] = mu;
+    n_keep[w] = keep.n;
   }
   __syncthreads();
-  S = Tt = 0.f;
+  int c = 0, at = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
-    S += warp_s[i];
-    Tt += warp_t[i];
+    mu = fmaxf(mu, red[0][i]);
+    if (i == w) at = c;
+    c += n_keep[i];
   }
-  const RowStats st = row_stats(m, S);
-  if (a.n_seg == 1) write_row(a, b, row.z, st, S, Tt);
-  else if (t == 0) a.part[blockIdx.x] = make_float4(m, S, Tt, 0.f);
+  s.move(mu);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+    s.T += __shfl_xor_sync(0xffffffffu, s.T, o);
+  }
+  if (inf) s.S = NAN;
+  if (lane == 0) {
+    red[1][w] = s.S;
+    red[2][w] = s.T;
+  }
+  if (c <= kCap)
+    for (int i = lane; i < keep.n; i += 32) flat[at + i] = keep_buf[w][i];
+  __syncthreads();
+  s.S = s.T = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    s.S += red[1][i];
+    s.T += red[2][i];
+  }
+  const RowStats st = row_stats(mu, s.S);
+  if (a.n_run == 1) write_row(a, b, row.z, st, s.S, s.T);
+  else if (t == 0) a.part[blockIdx.x] = make_float4(mu, s.S, s.T, 0.f);
   if (a.k == 0) return;
 
-  // the competing logits; a thread holds one only if its maximum does
-  auto collect = [&](auto keep) {
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int64_t j = row.column(v0 + i * kThreads);
-      float v[kE];
-      unpack<T>(raw[i], v);
-#pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (j + e >= 0 && j + e < a.N && keep(v[e], (uint32_t)(j + e))) {
-          const int at = atomicAdd(&n_cand, 1);
-          if (at < kCand) cand[at] = rank_key(v[e], (uint32_t)(j + e));
-        }
-    }
-  };
-  const bool odd = !(m == m);  // a NaN: the group maxima bound nothing
-  if (!odd) {
-    const float tau = tau_s;
-    if (mine >= tau) collect([&](float v, uint32_t) { return v >= tau; });
-  }
-  __syncthreads();
-  int c = n_cand;
-  if (odd || c > 256) {
-    uint64_t best[1] = {0};
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int64_t j = row.column(v0 + i * kThreads);
-      float v[kE];
-      unpack<T>(raw[i], v);
-#pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (j + e >= 0 && j + e < a.N) {
-          const uint64_t key = rank_key(v[e], (uint32_t)(j + e));
-          if (key > best[0]) best[0] = key;
-        }
-    }
-    const int live = __syncthreads_count(best[0] != 0);
-    const uint64_t tau = live > a.k ? kth_key(best, a.k) : 1;
-    __syncthreads();
-    if (t == 0) n_cand = 0;
-    __syncthreads();
-    if (best[0] >= tau) collect([&](float v, uint32_t id) { return rank_key(v, id) >= tau; });
-    __syncthreads();
-    c = n_cand;
-  }
   uint64_t* keys = a.keys + (int64_t)blockIdx.x * a.k;
   auto emit = [&](int rank, uint64_t key) {
-    if (a.n_seg == 1) {
+    if (a.n_run == 1) {
       a.top_id[b * a.k + rank] = (int32_t)key_id(key);
       a.top_logp[b * a.k + rank] = st.logp(key_value(key));
     } else {
       keys[rank] = key;
     }
   };
-  for (int i = t; i < c; i += kThreads) {
-    const uint64_t key = cand[i];
-    int rank = 0;
-    for (int j = 0; j < c; ++j) rank += cand[j] > key;
-    if (rank < a.k) emit(rank, key);
+  if (c <= kCap) {  // few: each counts the keys above it
+    if (t < c) {
+      const uint64_t key = flat[t];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < c; ++j) rank += flat[j] > key;
+      if (rank < a.k) emit(rank, key);
+    }
+    for (int r = c + t; r < a.k; r += kThreads) keys[r] = 0;  // a short last run
+  } else {
+    uint64_t key[kCap / 32];
+#pragma unroll
+    for (int i = 0; i < kCap / 32; ++i) key[i] = i * 32 + lane < keep.n ? keep_buf[w][i * 32 + lane] : 0;
+    emit_best(key, a.k, hist, found, best, &n_best, emit);
   }
-  if (a.n_seg > 1)  // a short last segment
-    for (int r = c + t; r < a.k; r += kThreads) keys[r] = 0;
 }
 
-// One CTA per row joins its segments.
+// One CTA per row joins its runs.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinCand = kMaxK * kMaxK;
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) k_logprob_join(Args a) {
+__global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
   __shared__ float red[3][kJoinThreads / 32];
-  __shared__ uint64_t cand[kJoinCand];
+  __shared__ uint64_t cand[kMaxK * kMaxK];
   __shared__ uint64_t best[kMaxK];
-  __shared__ int n_cand, n_best;
+  __shared__ int n_cand, n_best, hist[256], found[3];
   const int64_t b = blockIdx.x;
-  const int t = threadIdx.x, n = a.n_seg, k = a.k;
+  const int t = threadIdx.x, n = a.n_run, k = a.k;
   const float4* part = a.part + b * n;
-  float m = -INFINITY;
-  for (int i = t; i < n; i += kJoinThreads) m = max_nan(m, part[i].x);
+  constexpr int kPer = kMaxRuns / kJoinThreads;
+  float4 p[kPer];
+  float mu = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((t & 31) == 0) red[0][t >> 5] = m;
-  if (t == 0) n_cand = n_best = 0;
-  __syncthreads();
-  for (int i = 0; i < kJoinThreads / 32; ++i) m = max_nan(m, red[0][i]);
-  float S = 0.f, Tt = 0.f;
-  for (int i = t; i < n; i += kJoinThreads) {
-    const float4 p = part[i];
-    if (p.x > -INFINITY) {
-      const float d = p.x - m, w = expf(d);
-      S += w * p.y;
-      Tt += w * (p.z - p.y * fmaxf(d, -200.f));
-    }
+  for (int i = 0; i < kPer; ++i) {
+    p[i] = i * kJoinThreads + t < n ? part[i * kJoinThreads + t] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    mu = fmaxf(mu, p[i].x);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+  if ((t & 31) == 0) red[0][t >> 5] = mu;
+  if (t == 0) n_cand = 0;
+  __syncthreads();
+  for (int i = 0; i < kJoinThreads / 32; ++i) mu = fmaxf(mu, red[0][i]);
+  float S = 0.f, Tt = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (p[i].y != 0.f) {  // NaN too
+      Sums s{p[i].x, p[i].y, p[i].z};
+      s.move(mu);
+      S += s.S;
+      Tt += s.T;
+    }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     S += __shfl_xor_sync(0xffffffffu, S, o);
@@ -385,60 +589,59 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join(Args a) {
     S += red[1][i];
     Tt += red[2][i];
   }
-  const RowStats st = row_stats(m, S);
+  const RowStats st = row_stats(mu, S);
   write_row(a, b, static_cast<const T*>(a.logits) + b * a.N, st, S, Tt);
   if (k == 0) return;
-  // with more segments than alternatives, only the segments whose best is among the
-  // k best of the segments' bests hold any
+  // with more runs than alternatives, only the runs whose best is among the k best
+  // of the runs' bests hold any
   const uint64_t* keys = a.keys + b * n * k;
   uint64_t tau = 1;
   if (n > k) {
-    uint64_t top = 0;  // k-th largest of the heads, each thread's heads in turn
-    uint64_t lo = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t c = lo | (1ull << bit);
-      int cnt = 0;
-      for (int i0 = 0; i0 < n; i0 += kJoinThreads) cnt += __syncthreads_count(i0 + t < n && keys[(int64_t)(i0 + t) * k] >= c);
-      if (cnt >= k) lo = c;
-      if (cnt == k) break;
-    }
-    top = lo;
-    tau = top > 0 ? top : 1;
+    uint64_t head[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) head[i] = i * kJoinThreads + t < n ? keys[(int64_t)(i * kJoinThreads + t) * k] : 0;
+    tau = kth_key(head, k, hist, found);
+    __syncthreads();
   }
-  for (int64_t i = t; i < (int64_t)n * k; i += kJoinThreads) {
+  for (int i = t; i < n * k; i += kJoinThreads) {
     const uint64_t key = keys[i];
-    if (key >= tau) cand[atomicAdd(&n_cand, 1)] = key;
+    if (key != 0 && key >= tau) cand[atomicAdd(&n_cand, 1)] = key;
   }
   __syncthreads();
   const int c = n_cand;
-  constexpr int kPer = kJoinCand / kJoinThreads;
-  uint64_t mine[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) mine[i] = i * kJoinThreads + t < c ? cand[i * kJoinThreads + t] : 0;
-  const uint64_t last = kth_key(mine, k);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (mine[i] >= last && mine[i] != 0) best[atomicAdd(&n_best, 1)] = mine[i];
-  __syncthreads();
-  if (t < k) {
-    const uint64_t key = best[t];
-    int rank = 0;
-    for (int j = 0; j < k; ++j) rank += best[j] > key;
+  auto emit = [&](int rank, uint64_t key) {
     a.top_id[b * k + rank] = (int32_t)key_id(key);
     a.top_logp[b * k + rank] = st.logp(key_value(key));
+  };
+  if (c <= 256) {
+    if (t < c) {
+      const uint64_t key = cand[t];
+      int rank = 0;
+      for (int j = 0; j < c; ++j) rank += cand[j] > key;
+      if (rank < k) emit(rank, key);
+    }
+  } else {
+    uint64_t key[kMaxK * kMaxK / kJoinThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxK * kMaxK / kJoinThreads; ++i)
+      key[i] = i * kJoinThreads + t < c ? cand[i * kJoinThreads + t] : 0;
+    emit_best(key, k, hist, found, best, &n_best, emit);
   }
 }
 
-// One CTA per segment of a row: the dense term, then the given labels in it.
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8) k_logprob_grad(GradArgs a) {
+// One CTA per run of a row: the dense term of its blocks, then the given labels in
+// them.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   constexpr int kE = 16 / sizeof(T);
-  const int64_t b = blockIdx.x / a.n_seg;
-  const int seg = blockIdx.x % a.n_seg, t = threadIdx.x;
+  const int64_t b = blockIdx.x / a.n_run;
+  const int run = blockIdx.x % a.n_run, t = threadIdx.x;
   const Row<T> row(a.logits, b, a.N);
   T* dz = static_cast<T*>(a.d_logits) + b * a.N;
-  const int64_t v0 = (int64_t)seg * (kThreads * kV) + t;
+  const int n_blocks = (int)((a.N + row.head + kE * (int64_t)kBlock - 1) / (kE * (int64_t)kBlock));
+  const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
   uint4 raw[kV];
+  uint32_t v0 = (uint32_t)blk0 * kBlock + t;
 #pragma unroll
   for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
   const float lse = a.lse[b];
@@ -459,30 +662,42 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8) k_logprob_g
   };
   // the output may sit on the 16-byte boundary differently from the input
   const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+  for (int blk = blk0; blk < blk1; ++blk) {
+    uint4 cur[kV];
+    const uint32_t v_cur = v0;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int64_t j = row.column(v0 + i * kThreads);
-    if (j >= a.N) break;
-    float v[kE];
-    unpack<T>(raw[i], v);
+    for (int i = 0; i < kV; ++i) cur[i] = raw[i];
+    v0 += kBlock;
+    if (blk + 1 < blk1) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) v[e] = none ? 0.f : dense(v[e]);
-    if (vec && j >= 0 && j + kE <= a.N) {
-      uint4 o;
-      if constexpr (sizeof(T) == 2)
-        o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      else
-        o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-      *reinterpret_cast<uint4*>(dz + j) = o;
-    } else {
+      for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
+    }
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
+    for (int i = 0; i < kV; ++i) {
+      const int64_t j = row.column(v_cur + i * kThreads);
+      if (j >= a.N) break;
+      float v[kE];
+      unpack<T>(cur[i], v);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[e] = none ? 0.f : dense(v[e]);
+      if (vec && row.whole(j)) {
+        uint4 o;
+        if constexpr (sizeof(T) == 2)
+          o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        else
+          o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        *reinterpret_cast<uint4*>(dz + j) = o;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+          if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
+      }
     }
   }
   if (p0 == p1 || none) return;
   __syncthreads();
-  const int64_t c0 = row.column((int64_t)seg * (kThreads * kV)), c1 = c0 + (int64_t)kThreads * kV * kE;
+  const int64_t c0 = row.column((uint32_t)blk0 * kBlock), c1 = row.column((uint32_t)blk1 * kBlock);
   for (int64_t p = p0 + t; p < p1; p += kThreads) {
     const int64_t id = a.ids[p];
     if (id < 0 || id >= a.N || id < c0 || id >= c1) continue;
@@ -497,18 +712,24 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8) k_logprob_g
   }
 }
 
-// Threads of a segment's CTA: rows that 128 threads hold whole take one such CTA.
-inline int seg_threads(int64_t vectors) { return vectors <= 128 * kV ? 128 : 512; }
-inline int64_t segments(int64_t vectors) {
-  const int64_t per = (int64_t)seg_threads(vectors) * kV;
-  return (vectors + per - 1) / per;
+// Blocks that a row of N elements can touch, wherever it starts.
+template <typename T>
+inline int64_t row_blocks(int64_t N) {
+  constexpr int64_t kE = 16 / sizeof(T);
+  return (N + 2 * kE - 2) / (kE * kBlock) + 1;
 }
+// Runs of a row: enough CTAs for some waves, at least a block each.
+inline int64_t runs(int B, int64_t blocks, int64_t ctas) {
+  if (B >= 128 && blocks <= 4) return 1;
+  const int64_t want = (ctas + B - 1) / B;
+  const int64_t n = blocks < want ? blocks : want;
+  return n < 1 ? 1 : n > kMaxRuns ? kMaxRuns : n;
+}
+constexpr int kCtas = 1776, kGradCtas = 1776;
 
 template <typename T>
-cudaError_t launch(int B, int threads, const Args& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)B * a.n_seg);
-  if (threads == 128) k_logprob<T, 128><<<grid, 128, 0, st>>>(a);
-  else k_logprob<T, 512><<<grid, 512, 0, st>>>(a);
+cudaError_t launch(int B, const Args& a, cudaStream_t st) {
+  k_logprob<T><<<(unsigned)(B * (int64_t)a.n_run), kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
@@ -516,12 +737,9 @@ cudaError_t launch_join(int B, const Args& a, cudaStream_t st) {
   k_logprob_join<T><<<B, kJoinThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
-
 template <typename T>
-cudaError_t launch_grad(int B, int threads, const GradArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)B * a.n_seg);
-  if (threads == 128) k_logprob_grad<T, 128><<<grid, 128, 0, st>>>(a);
-  else k_logprob_grad<T, 512><<<grid, 512, 0, st>>>(a);
+cudaError_t launch_grad(int B, const GradArgs& a, cudaStream_t st) {
+  k_logprob_grad<T><<<(unsigned)(B * (int64_t)a.n_run), kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
