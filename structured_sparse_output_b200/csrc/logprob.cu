@@ -14,12 +14,14 @@
 namespace haste {
 namespace logprob {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxK = 64;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kV = 4;                     // 16-byte vectors of a thread in a block of a row
 constexpr int kBlock = kThreads * kV;     // vectors of a block: 16 KB of a row
-constexpr int kCap = 256;                 // competing logits that a warp keeps
+constexpr int kCap = 128;                 // competing logits that a warp keeps
+constexpr int kRoom = 96;                 // and how many at most after it drops some
+constexpr int kDepth = 6;                 // vectors of a thread in flight or waiting
 constexpr int kMaxRuns = 1024;            // runs of a row
 
 struct Args {
@@ -35,7 +37,7 @@ struct Args {
   float* entropy;
   float* top_logp;
   int32_t* top_id;
-  float4* part;    // [B, n_run] (m, S, T): the runs' sums when n_run > 1
+  float4* part;    // [B, n_run] (mu, S, Y): the runs' sums when n_run > 1
   uint64_t* keys;  // [B, n_run, k] rank keys of the run's best, descending, 0 = none
 };
 
@@ -75,10 +77,38 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
+__device__ __forceinline__ float ex2(float x) {  // 2^x, 0 below the normal numbers
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// Two fp32 numbers in one register pair: one instruction adds or multiplies both.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 p) {
+  float a, b;
+  unpair(p, a, b);
+  return pair(ex2(a), ex2(b));
 }
 
 // The given labels of row b: [begin, end) of the lists, within [0, nnz] whatever
@@ -226,7 +256,7 @@ struct Keep {
   uint64_t tau;
 };
 
-// Raise tau until at most kCap / 2 of the warp's keys reach it, and still k do.
+// Raise tau until at most kRoom of the warp's keys reach it, and still k do.
 __device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
   const int lane = threadIdx.x & 31;
   uint64_t key[kCap / 32];
@@ -240,7 +270,7 @@ __device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
 #pragma unroll
     for (int i = 0; i < kCap / 32; ++i) cnt += __popc(__ballot_sync(0xffffffffu, key[i] >= up));
     if (cnt >= k) c = up;
-    if (cnt >= k && cnt <= kCap / 2) break;
+    if (cnt >= k && cnt <= kRoom) break;
   }
   int at = 0;
   __syncwarp();
@@ -255,12 +285,19 @@ __device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
   return Keep{at, c > s.tau ? c : s.tau};
 }
 
-// Add the logits of one vector of every lane that reach tau; hit: bits of the
-// lane's elements whose value does (or all of them, where tau's value is -inf).
+// Add the logits of one vector of every lane that reach tau (tau_f is its value; a
+// NaN counts as -inf).
 template <typename T>
-__device__ __forceinline__ Keep take(uint64_t* buf, Keep s, const uint4& raw, uint32_t hit, int64_t j, uint32_t N,
-                                     int k) {
+__device__ __noinline__ Keep take(uint64_t* buf, Keep s, uint4 raw, float tau_f, int64_t j, uint32_t N, int k) {
+  constexpr int kE = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
+  uint32_t hit = 0;
+  {
+    float v[kE];
+    unpack<T>(raw, v);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) hit |= (v[e] >= tau_f || tau_f == -INFINITY) ? 1u << e : 0u;
+  }
   while (__any_sync(0xffffffffu, hit != 0)) {
     uint64_t key = 0;
     if (hit) {
@@ -327,90 +364,121 @@ __device__ void emit_best(const uint64_t (&key)[kN], int k, int* hist, int* foun
   }
 }
 
-// Sums of one thread, warp or block around a reference mu (finite): S = sum
-// e^(z - mu), T = sum e^(z - mu) (mu - z).
+// References beyond it take y = (z - mu) log2(e): R would lose more than 2^-7.
+constexpr float kFar = 65536.f;
+
+// Sums around a finite reference mu, in powers of two: y = z log2(e) - R with R =
+// fl(mu log2(e)), S = sum 2^y, Y = sum 2^y y.  One fused multiply-add gives y; what R
+// lost in rounding is put back once, by settle().
 struct Sums {
-  float mu, S, T;
+  float mu, R, S, Y;
+  __device__ explicit Sums(float m) : mu(m), R(m * kLog2e), S(0.f), Y(0.f) {}
   __device__ void move(float to) {  // to >= mu
-    const float d = fmaxf(mu - to, -200.f), w = ex2(d * kLog2e);
-    T = w * fmaf(-S, d, T);
+    const float r = to * kLog2e;
+    const float d = fmaxf(fabsf(mu) < kFar && fabsf(to) < kFar ? R - r : (mu - to) * kLog2e, -300.f), w = ex2(d);
+    Y = w * fmaf(S, d, Y);
     S *= w;
     mu = to;
+    R = r;
+  }
+  // S = sum e^(z - mu) and T = sum e^(z - mu) (mu - z)
+  __device__ float settle() {
+    const float d = fabsf(mu) < kFar ? fmaf(mu, kLog2e, -R) : 0.f, w = ex2(-d);
+    S *= w;
+    return -kLn2 * fmaf(-d, S, w * Y);
   }
 };
 
-// -inf counts as `lo`, whose e^(lo - mu) is 0 in fp32: the sums then meet no
-// infinity times 0.  A multiple of mu goes into the distance so that lo differs from
-// mu in bf16, too.
+// -inf counts as `lo`, whose 2^y is 0: the sums then meet no infinity times 0.  A
+// multiple of mu goes into the distance so that lo differs from mu in bf16, too.
 __device__ __forceinline__ float floor_of(float mu) { return mu - fmaxf(200.f, 0.02f * fabsf(mu)); }
-constexpr float kDeep = -3.2e38f;  // no such floor exists below it
 
-// The sums of one vector.  Logits are raised to the floor before they are widened:
-// two at a time in bf16 (max keeps a NaN).
-template <typename T, bool kIsDeep>
-__device__ __forceinline__ void sum_vector(Sums& s, const uint4& raw, float lo) {
-  constexpr int kE = 16 / sizeof(T);
-  float v[kE];
-  if constexpr (sizeof(T) == 2 && !kIsDeep) {
+// A vector's logits as pairs, raised to the floor before they are widened: two at a
+// time in bf16 (max keeps a NaN).
+template <typename T>
+__device__ __forceinline__ void raised(const uint4& raw, float lo, f2 (&v)[8 / sizeof(T)]) {
+  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (sizeof(T) == 2) {
     const __nv_bfloat162 lo2 = __float2bfloat162_rn(lo);
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&u[i]), lo2);
-      c[i] = *reinterpret_cast<const uint32_t*>(&r);
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(&r);
+      v[i] = pair(__uint_as_float(c << 16), __uint_as_float(c & 0xffff0000u));
     }
-    unpack<T>(make_uint4(c[0], c[1], c[2], c[3]), v);
   } else {
-    unpack<T>(raw, v);
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
-      if (!kIsDeep) v[e] = max_nan(v[e], lo);
+    for (int i = 0; i < 2; ++i)
+      v[i] = pair(max_nan(__uint_as_float(u[2 * i]), lo), max_nan(__uint_as_float(u[2 * i + 1]), lo));
   }
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    float d = v[e] - s.mu;
-    if (kIsDeep) d = max_nan(d, -200.f);
-    const float x = ex2(d * kLog2e);
-    s.S += x;
-    s.T = fmaf(-x, d, s.T);
+}
+// The largest logit of a vector; NaN is passed over.
+template <typename T>
+__device__ __forceinline__ float vector_max(const uint4& r) {
+  if constexpr (sizeof(T) == 2) {
+    auto h = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(h(r.x), h(r.y)), __hmax2(h(r.z), h(r.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
 }
 
-// One CTA per run of a row: blocks of 256 threads x 64 bytes, the next block's
-// loads in flight while one is summed.  The threads' maxima bound the k-th best
-// logit from below, over the first block and again after 2, 4, 8 .. blocks; a warp
-// looks at single logits only where a vector's maximum reaches the bound.
+// The sums of one vector around a reference beyond kFar, and before any is known.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) k_logprob(Args a) {
+__device__ __noinline__ float2 far_sums(uint4 raw, float mu) {
   constexpr int kE = 16 / sizeof(T);
+  float v[kE], S = 0.f, Y = 0.f;
+  unpack<T>(raw, v);
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    const float y = max_nan((v[e] - mu) * kLog2e, -300.f), x = ex2(y);
+    S += x;
+    Y = fmaf(x, y, Y);
+  }
+  return make_float2(S, Y);
+}
+
+// One CTA per run of a row, in steps of one vector a thread; every thread copies its
+// vectors of the next steps into its own slots of shared memory (cp.async, no
+// barrier), which costs no registers.  The threads' maxima bound the k-th best logit
+// from below, over the first block of kV steps and again after 2, 4, 8 .. blocks; a
+// warp looks at single logits only where a vector's maximum reaches the bound.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 5) k_logprob(Args a) {
+  constexpr int kE = 16 / sizeof(T), kP = kE / 2;
+  __shared__ uint4 ring[kDepth][kThreads];
   __shared__ float red[3][kWarps];
   __shared__ __align__(16) uint32_t group[128];
   __shared__ uint32_t tau_s;
   __shared__ int n_keep[kWarps], hist[256], found[3], n_best;
-  __shared__ uint64_t keep_buf[kWarps][kCap], flat[kCap];
+  __shared__ uint64_t keep_buf[kWarps][kCap], flat[kThreads];
   __shared__ uint64_t best[kMaxK];
   const int64_t b = blockIdx.x / a.n_run;
   const int run = blockIdx.x % a.n_run, t = threadIdx.x, w = t >> 5, lane = t & 31;
   const Row<T> row(a.logits, b, a.N);
   const int n_blocks = (int)((a.N + row.head + kE * (int64_t)kBlock - 1) / (kE * (int64_t)kBlock));
   const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
-
-  uint4 raw[kV];
-  uint32_t v0 = (uint32_t)blk0 * kBlock + t;
-#pragma unroll
-  for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
-  auto vector_max = [](const uint4& r) {  // NaN is ignored here; it ends up in S
-    float v[kE];
-    unpack<T>(r, v);
-    float m = v[0];
-#pragma unroll
-    for (int e = 1; e < kE; ++e) m = fmaxf(m, v[e]);
-    return m;
+  const int n = (blk1 - blk0) * kV;  // steps
+  const uint32_t v0 = (uint32_t)blk0 * kBlock + t;
+  // steps [in0, in1) lie whole inside the row
+  const int in0 = blk0 == 0 && row.head ? 1 : 0;
+  const int in1 = (int)((a.N + row.head) / (kE * (int64_t)kThreads) - (int64_t)blk0 * kV);
+  const uint4* src = reinterpret_cast<const uint4*>(row.z - row.head) + v0;
+  auto request = [&](int i, int slot) {
+    if (i < n) {
+      if (i >= in0 && i < in1) cp_async16(smem_u32(&ring[slot][t]), src + (int64_t)i * kThreads, 16);
+      else ring[slot][t] = row.load(v0 + (uint32_t)i * kThreads);
+    }
+    cp_async_commit();
   };
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) request(i, i);
+  cp_async_wait_group<kDepth - 1 - kV>();
   float mx = -INFINITY;  // of what this thread has seen
 #pragma unroll
-  for (int i = 0; i < kV; ++i) mx = fmaxf(mx, vector_max(raw[i]));
+  for (int i = 0; i < kV; ++i)
+    if (i < n) mx = fmaxf(mx, vector_max<T>(ring[i][t]));
   auto bound = [&] { return a.k <= 16 ? bound_of<64>(mx, a.k, group, &tau_s) : bound_of<128>(mx, a.k, group, &tau_s); };
   float m = mx;
 #pragma unroll
@@ -426,50 +494,68 @@ __global__ void __launch_bounds__(kThreads, 3) k_logprob(Args a) {
   }
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) m = fmaxf(m, red[0][i]);
-  Sums s{m < INFINITY ? fmaxf(m, -FLT_MAX) : 0.f, 0.f, 0.f};
+  Sums s(m < INFINITY ? fmaxf(m, -FLT_MAX) : 0.f);
+  f2 S2 = 0, Y2 = 0;  // two sums each, of a block at most
+  auto gather = [&] {
+    float x, y;
+    unpair(S2, x, y);
+    s.S += x + y;
+    unpair(Y2, x, y);
+    s.Y += x + y;
+    S2 = Y2 = 0;
+  };
   float lo = floor_of(s.mu);
   bool inf = !(m < INFINITY);
 
-  for (int blk = blk0; blk < blk1; ++blk) {
-    uint4 cur[kV];
-    const uint32_t v_cur = v0;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) cur[i] = raw[i];
-    v0 += kBlock;
-    if (blk + 1 < blk1) {
-#pragma unroll
-      for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
-    }
-    const int seen = blk - blk0;
-    if (a.k > 0 && seen >= 2 && (seen & (seen - 1)) == 0) {
-      const uint64_t up = (uint64_t)bound() << 32;
-      if (up > keep.tau) {
-        keep.tau = up;
-        tau_f = key_value(up);
+  int slot = 0, next = kDepth - 1;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    if (i % kV == 0) {
+      gather();
+      const int seen = i / kV;
+      if (a.k > 0 && seen >= 2 && (seen & (seen - 1)) == 0) {
+        const uint64_t up = (uint64_t)bound() << 32;
+        if (up > keep.tau) {
+          keep.tau = up;
+          tau_f = key_value(up);
+        }
       }
     }
+    cp_async_wait_group<kDepth - 2>();
+    const uint4 cur = ring[slot][t];
+    request(i + kDepth - 1, next);
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    next = next + 1 == kDepth ? 0 : next + 1;
+    const float vm = vector_max<T>(cur);
+    mx = fmaxf(mx, vm);
+    if (vm > s.mu) {
+      gather();
+      if (vm < INFINITY) s.move(vm);
+      else inf = true;
+      lo = floor_of(s.mu);
+    }
+    if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0) {
+      keep = take<T>(keep_buf[w], keep, cur, tau_f, row.column(v0 + (uint32_t)i * kThreads), row.N, a.k);
+      tau_f = key_value(keep.tau);
+    }
+    if (fabsf(s.mu) < kFar) {
+      f2 v[kP];
+      raised<T>(cur, lo, v);
+      const f2 L = pair(kLog2e, kLog2e), R = pair(-s.R, -s.R);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const float vm = vector_max(cur[i]);
-      mx = fmaxf(mx, vm);
-      if (vm > s.mu) {
-        if (vm < INFINITY) s.move(vm);
-        else inf = true;
-        lo = floor_of(s.mu);
+      for (int e = 0; e < kP; ++e) {
+        const f2 y = fma2(v[e], L, R), x = ex2_2(y);
+        S2 = add2(S2, x);
+        Y2 = fma2(x, y, Y2);
       }
-      if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0) {
-        float v[kE];
-        unpack<T>(cur[i], v);
-        uint32_t hit = 0;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) hit |= (v[e] >= tau_f || tau_f == -INFINITY) ? 1u << e : 0u;
-        keep = take<T>(keep_buf[w], keep, cur[i], hit, row.column(v_cur + i * kThreads), row.N, a.k);
-        tau_f = key_value(keep.tau);
-      }
-      if (s.mu > kDeep) sum_vector<T, false>(s, cur[i], lo);
-      else sum_vector<T, true>(s, cur[i], lo);
+    } else {
+      const float2 r = far_sums<T>(cur, s.mu);
+      s.S += r.x;
+      s.Y += r.y;
     }
   }
+  cp_async_wait_all();
+  gather();
 
   // join the threads' sums around the run's maximum
   float mu = s.mu;
@@ -493,25 +579,26 @@ __global__ void __launch_bounds__(kThreads, 3) k_logprob(Args a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
-    s.T += __shfl_xor_sync(0xffffffffu, s.T, o);
+    s.Y += __shfl_xor_sync(0xffffffffu, s.Y, o);
   }
   if (inf) s.S = NAN;
   if (lane == 0) {
     red[1][w] = s.S;
-    red[2][w] = s.T;
+    red[2][w] = s.Y;
   }
-  if (c <= kCap)
+  if (c <= kThreads)
     for (int i = lane; i < keep.n; i += 32) flat[at + i] = keep_buf[w][i];
   __syncthreads();
-  s.S = s.T = 0.f;
+  s.S = s.Y = 0.f;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     s.S += red[1][i];
-    s.T += red[2][i];
+    s.Y += red[2][i];
   }
+  if (a.n_run > 1 && t == 0) a.part[blockIdx.x] = make_float4(mu, s.S, s.Y, 0.f);
+  const float Tt = s.settle();
   const RowStats st = row_stats(mu, s.S);
-  if (a.n_run == 1) write_row(a, b, row.z, st, s.S, s.T);
-  else if (t == 0) a.part[blockIdx.x] = make_float4(mu, s.S, s.T, 0.f);
+  if (a.n_run == 1) write_row(a, b, row.z, st, s.S, Tt);
   if (a.k == 0) return;
 
   uint64_t* keys = a.keys + (int64_t)blockIdx.x * a.k;
@@ -523,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_logprob(Args a) {
       keys[rank] = key;
     }
   };
-  if (c <= kCap) {  // few: each counts the keys above it
+  if (c <= kThreads) {  // few: each counts the keys above it
     if (t < c) {
       const uint64_t key = flat[t];
       int rank = 0;
@@ -531,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_logprob(Args a) {
       for (int j = 0; j < c; ++j) rank += flat[j] > key;
       if (rank < a.k) emit(rank, key);
     }
-    for (int r = c + t; r < a.k; r += kThreads) keys[r] = 0;  // a short last run
+    if (a.n_run > 1)  // a short last run
+      for (int r = c + t; r < a.k; r += kThreads) keys[r] = 0;
   } else {
     uint64_t key[kCap / 32];
 #pragma unroll
@@ -565,32 +653,35 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
   if (t == 0) n_cand = 0;
   __syncthreads();
   for (int i = 0; i < kJoinThreads / 32; ++i) mu = fmaxf(mu, red[0][i]);
-  float S = 0.f, Tt = 0.f;
+  Sums s(mu);
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     if (p[i].y != 0.f) {  // NaN too
-      Sums s{p[i].x, p[i].y, p[i].z};
-      s.move(mu);
-      S += s.S;
-      Tt += s.T;
+      Sums r(p[i].x);
+      r.S = p[i].y;
+      r.Y = p[i].z;
+      r.move(mu);
+      s.S += r.S;
+      s.Y += r.Y;
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    S += __shfl_xor_sync(0xffffffffu, S, o);
-    Tt += __shfl_xor_sync(0xffffffffu, Tt, o);
+    s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+    s.Y += __shfl_xor_sync(0xffffffffu, s.Y, o);
   }
   if ((t & 31) == 0) {
-    red[1][t >> 5] = S;
-    red[2][t >> 5] = Tt;
+    red[1][t >> 5] = s.S;
+    red[2][t >> 5] = s.Y;
   }
   __syncthreads();
-  S = Tt = 0.f;
+  s.S = s.Y = 0.f;
   for (int i = 0; i < kJoinThreads / 32; ++i) {
-    S += red[1][i];
-    Tt += red[2][i];
+    s.S += red[1][i];
+    s.Y += red[2][i];
   }
-  const RowStats st = row_stats(mu, S);
-  write_row(a, b, static_cast<const T*>(a.logits) + b * a.N, st, S, Tt);
+  const float Tt = s.settle();
+  const RowStats st = row_stats(mu, s.S);
+  write_row(a, b, static_cast<const T*>(a.logits) + b * a.N, st, s.S, Tt);
   if (k == 0) return;
   // with more runs than alternatives, only the runs whose best is among the k best
   // of the runs' bests hold any
@@ -630,20 +721,23 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
 }
 
 // One CTA per run of a row: the dense term of its blocks, then the given labels in
-// them.
+// them.  With y = z log2(e) - R, R = fl(lse log2(e)) and e = lse log2(e) - R, which an
+// fma gives exactly, p = 2^(y - e) and log p = ln2 (y - e): the dense term is
+// -2^y (A + C y) with A and C of the row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
-  constexpr int kE = 16 / sizeof(T);
+  constexpr int kE = 16 / sizeof(T), kP = kE / 2;
   const int64_t b = blockIdx.x / a.n_run;
   const int run = blockIdx.x % a.n_run, t = threadIdx.x;
   const Row<T> row(a.logits, b, a.N);
   T* dz = static_cast<T*>(a.d_logits) + b * a.N;
   const int n_blocks = (int)((a.N + row.head + kE * (int64_t)kBlock - 1) / (kE * (int64_t)kBlock));
   const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
+  const int in0 = row.head ? 1 : 0, in1 = (int)((a.N + row.head) / (kE * (int64_t)kBlock));
+  const uint4* at_row = reinterpret_cast<const uint4*>(row.z - row.head) + t;
   uint4 raw[kV];
-  uint32_t v0 = (uint32_t)blk0 * kBlock + t;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
+  for (int i = 0; i < kV; ++i) raw[i] = row.load((uint32_t)blk0 * kBlock + t + i * kThreads);
   const float lse = a.lse[b];
   const bool none = lse == -INFINITY;
   const float gH = a.d_entropy ? a.d_entropy[b] : 0.f, H = a.d_entropy ? a.entropy[b] : 0.f;
@@ -656,39 +750,51 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
+  // the definition, for single labels and where R would lose too much
   auto dense = [&](float v) {
     const float lp = v - lse, p = ex2(lp * kLog2e);
-    return p == 0.f ? 0.f : -p * fmaf(gH, lp + H, G);
+    return p == 0.f || none ? 0.f : -p * fmaf(gH, lp + H, G);
   };
+  const bool near = fabsf(lse) < kFar || lse != lse;
+  const float R = lse * kLog2e, e0 = fmaf(lse, kLog2e, -R), w = -ex2(-e0), lo = floor_of(lse);
+  const float A = w * fmaf(gH, fmaf(-kLn2, e0, H), G), C = w * gH * kLn2;
+  const f2 L2 = pair(kLog2e, kLog2e), R2 = pair(-R, -R), A2 = pair(A, A), C2 = pair(C, C);
   // the output may sit on the 16-byte boundary differently from the input
   const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+  uint4* out_row = reinterpret_cast<uint4*>(dz - row.head) + t;
   for (int blk = blk0; blk < blk1; ++blk) {
-    uint4 cur[kV];
-    const uint32_t v_cur = v0;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) cur[i] = raw[i];
-    v0 += kBlock;
-    if (blk + 1 < blk1) {
-#pragma unroll
-      for (int i = 0; i < kV; ++i) raw[i] = row.load(v0 + i * kThreads);
-    }
+    const bool more = blk + 1 < blk1, inside = blk + 1 >= in0 && blk + 1 < in1;
+    const bool whole = vec && blk >= in0 && blk < in1;
+    const uint32_t v0 = (uint32_t)blk * kBlock + t;
+    const uint4* next = at_row + (int64_t)(blk + 1) * kBlock;
+    uint4* out = out_row + (int64_t)blk * kBlock;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-      const int64_t j = row.column(v_cur + i * kThreads);
-      if (j >= a.N) break;
       float v[kE];
-      unpack<T>(cur[i], v);
+      if (near) {
+        f2 x[kP];
+        raised<T>(raw[i], lo, x);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) v[e] = none ? 0.f : dense(v[e]);
-      if (vec && row.whole(j)) {
+        for (int e = 0; e < kP; ++e) {
+          const f2 y = fma2(x[e], L2, R2);
+          unpair(mul2(ex2_2(y), fma2(y, C2, A2)), v[2 * e], v[2 * e + 1]);
+        }
+      } else {
+        unpack<T>(raw[i], v);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) v[e] = dense(v[e]);
+      }
+      if (more) raw[i] = inside ? next[i * kThreads] : row.load(v0 + kBlock + i * kThreads);
+      if (whole) {
         uint4 o;
         if constexpr (sizeof(T) == 2)
           o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                          pack_bf16x2(v[6], v[7]));
         else
           o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        *reinterpret_cast<uint4*>(dz + j) = o;
+        out[i * kThreads] = o;
       } else {
+        const int64_t j = row.column(v0 + i * kThreads);
 #pragma unroll
         for (int e = 0; e < kE; ++e)
           if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
