@@ -21,7 +21,8 @@ constexpr int kV = 4;                     // 16-byte vectors of a thread in a bl
 constexpr int kBlock = kThreads * kV;     // vectors of a block: 16 KB of a row
 constexpr int kCap = 128;                 // competing logits that a warp keeps
 constexpr int kRoom = 96;                 // and how many at most after it drops some
-constexpr int kDepth = 6;                 // vectors of a thread in flight or waiting
+constexpr int kRing = 2;                  // blocks in flight or in use
+constexpr int kList = 128;                // vectors that a warp notes before it looks into them
 constexpr int kMaxRuns = 1024;            // runs of a row
 
 struct Args {
@@ -285,14 +286,15 @@ __device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
   return Keep{at, c > s.tau ? c : s.tau};
 }
 
-// Add the logits of one vector of every lane that reach tau (tau_f is its value; a
-// NaN counts as -inf).
+// Add the logits of one vector of every lane (of those with `live`) that reach tau; a
+// NaN counts as -inf.
 template <typename T>
-__device__ __noinline__ Keep take(uint64_t* buf, Keep s, uint4 raw, float tau_f, int64_t j, uint32_t N, int k) {
+__device__ __noinline__ Keep take(uint64_t* buf, Keep s, uint4 raw, bool live, int64_t j, uint32_t N, int k) {
   constexpr int kE = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   uint32_t hit = 0;
-  {
+  if (live) {
+    const float tau_f = key_value(s.tau);
     float v[kE];
     unpack<T>(raw, v);
 #pragma unroll
@@ -412,15 +414,22 @@ __device__ __forceinline__ void raised(const uint4& raw, float lo, f2 (&v)[8 / s
       v[i] = pair(max_nan(__uint_as_float(u[2 * i]), lo), max_nan(__uint_as_float(u[2 * i + 1]), lo));
   }
 }
-// The largest logit of a vector; NaN is passed over.
-template <typename T>
-__device__ __forceinline__ float vector_max(const uint4& r) {
+// The largest logit of kN vectors; NaN is passed over.
+template <typename T, int kN>
+__device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
   if constexpr (sizeof(T) == 2) {
     auto h = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(h(r.x), h(r.y)), __hmax2(h(r.z), h(r.w)));
+    __nv_bfloat162 m = h(r[0].x);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) m = __hmax2(m, __hmax2(__hmax2(h(r[i].x), h(r[i].y)), __hmax2(h(r[i].z), h(r[i].w))));
     return fmaxf(__low2float(m), __high2float(m));
   } else {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)),
+                         fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
+    return m;
   }
 }
 
@@ -439,123 +448,166 @@ __device__ __noinline__ float2 far_sums(uint4 raw, float mu) {
   return make_float2(S, Y);
 }
 
-// One CTA per run of a row, in steps of one vector a thread; every thread copies its
-// vectors of the next steps into its own slots of shared memory (cp.async, no
-// barrier), which costs no registers.  The threads' maxima bound the k-th best logit
-// from below, over the first block of kV steps and again after 2, 4, 8 .. blocks; a
-// warp looks at single logits only where a vector's maximum reaches the bound.
+// Look into the vectors that a warp noted (numbers within the run, which starts at
+// vector v0 of the row): those from `kept` on are still in the ring.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5) k_logprob(Args a) {
+__device__ __noinline__ Keep look(uint64_t* buf, Keep s, const uint32_t* list, int n_list, const Row<T> row, uint32_t v0,
+                                  const uint4* ring, uint32_t kept, int k) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  for (int i = 0; i < n_list; i += 32) {
+    const bool live = i + lane < n_list;
+    const uint32_t at = list[live ? i + lane : i], v = v0 + at;
+    s = take<T>(buf, s, at >= kept ? ring[at % (kRing * kBlock)] : row.load(v), live, row.column(v), row.N, k);
+  }
+  __syncwarp();
+  return s;
+}
+
+// One CTA per run of a row, block by block; every thread copies its vectors of the
+// next block into its own slots of shared memory (cp.async, no barrier), which costs
+// no registers.  The threads' maxima bound the k-th best logit from below: over the
+// first block, again after 2, 4, 8 .. blocks and at the end.  A warp notes the vectors
+// whose maximum reaches the bound of the time, and looks into them at the end (or
+// when its list is full), when the bound has left few.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   constexpr int kE = 16 / sizeof(T), kP = kE / 2;
-  __shared__ uint4 ring[kDepth][kThreads];
+  __shared__ uint4 ring[kRing][kV][kThreads];
   __shared__ float red[3][kWarps];
   __shared__ __align__(16) uint32_t group[128];
   __shared__ uint32_t tau_s;
   __shared__ int n_keep[kWarps], hist[256], found[3], n_best;
-  __shared__ uint64_t keep_buf[kWarps][kCap], flat[kThreads];
+  __shared__ uint64_t keep_buf[kWarps][kCap];
+  __shared__ uint32_t noted[kWarps][kList];
   __shared__ uint64_t best[kMaxK];
   const int64_t b = blockIdx.x / a.n_run;
   const int run = blockIdx.x % a.n_run, t = threadIdx.x, w = t >> 5, lane = t & 31;
   const Row<T> row(a.logits, b, a.N);
   const int n_blocks = (int)((a.N + row.head + kE * (int64_t)kBlock - 1) / (kE * (int64_t)kBlock));
   const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
-  const int n = (blk1 - blk0) * kV;  // steps
-  const uint32_t v0 = (uint32_t)blk0 * kBlock + t;
-  // steps [in0, in1) lie whole inside the row
-  const int in0 = blk0 == 0 && row.head ? 1 : 0;
-  const int in1 = (int)((a.N + row.head) / (kE * (int64_t)kThreads) - (int64_t)blk0 * kV);
+  const uint32_t run0 = (uint32_t)blk0 * kBlock, v0 = run0 + t;
+  // blocks [in0, in1) lie whole inside the row
+  const int in0 = row.head ? 1 : 0, in1 = (int)((a.N + row.head) / (kE * (int64_t)kBlock));
   const uint4* src = reinterpret_cast<const uint4*>(row.z - row.head) + v0;
-  auto request = [&](int i, int slot) {
-    if (i < n) {
-      if (i >= in0 && i < in1) cp_async16(smem_u32(&ring[slot][t]), src + (int64_t)i * kThreads, 16);
-      else ring[slot][t] = row.load(v0 + (uint32_t)i * kThreads);
+  uint32_t v_next = v0;  // vector of the next request
+  auto request = [&](int blk) {
+    if (blk < blk1) {
+      uint4(*to)[kThreads] = ring[(blk - blk0) % kRing];
+      if (blk >= in0 && blk < in1) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) cp_async16(smem_u32(&to[i][t]), src + i * kThreads, 16);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kV; ++i) to[i][t] = row.load(v_next + i * kThreads);
+      }
+      src += kBlock;
+      v_next += kBlock;
     }
     cp_async_commit();
   };
+  request(blk0);
+  request(blk0 + 1);
+  cp_async_wait_group<1>();
+  uint4 cur[kV];
+  float vm;  // of this thread's vectors of the block
+  auto read = [&](int blk) {
+    uint4(*at)[kThreads] = ring[(blk - blk0) % kRing];
 #pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) request(i, i);
-  cp_async_wait_group<kDepth - 1 - kV>();
-  float mx = -INFINITY;  // of what this thread has seen
-#pragma unroll
-  for (int i = 0; i < kV; ++i)
-    if (i < n) mx = fmaxf(mx, vector_max<T>(ring[i][t]));
+    for (int i = 0; i < kV; ++i) cur[i] = at[i][t];
+    vm = max_of<T>(cur);
+  };
+  read(blk0);
+  float mx = blk0 < blk1 ? vm : -INFINITY;  // of what this thread has seen
   auto bound = [&] { return a.k <= 16 ? bound_of<64>(mx, a.k, group, &tau_s) : bound_of<128>(mx, a.k, group, &tau_s); };
   float m = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[0][w] = m;
-  Keep keep{0, ~0ull};
+  Keep keep{0, 0};
   float tau_f = INFINITY;
-  if (a.k > 0) {
-    keep.tau = (uint64_t)bound() << 32;
+  auto raise = [&] {
+    const uint64_t up = (uint64_t)bound() << 32;
+    if (up > keep.tau) keep.tau = up;
     tau_f = key_value(keep.tau);
-  } else {
-    __syncthreads();
-  }
+  };
+  if (a.k > 0) raise();
+  else __syncthreads();
+  int n_noted = 0, seen_by_bound = 1;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) m = fmaxf(m, red[0][i]);
   Sums s(m < INFINITY ? fmaxf(m, -FLT_MAX) : 0.f);
-  f2 S2 = 0, Y2 = 0;  // two sums each, of a block at most
-  auto gather = [&] {
-    float x, y;
-    unpair(S2, x, y);
-    s.S += x + y;
-    unpair(Y2, x, y);
-    s.Y += x + y;
-    S2 = Y2 = 0;
-  };
   float lo = floor_of(s.mu);
   bool inf = !(m < INFINITY);
 
-  int slot = 0, next = kDepth - 1;
 #pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    if (i % kV == 0) {
-      gather();
-      const int seen = i / kV;
-      if (a.k > 0 && seen >= 2 && (seen & (seen - 1)) == 0) {
-        const uint64_t up = (uint64_t)bound() << 32;
-        if (up > keep.tau) {
-          keep.tau = up;
-          tau_f = key_value(up);
-        }
+  for (int blk = blk0; blk < blk1; ++blk) {
+    if (blk > blk0) {
+      cp_async_wait_group<1>();
+      read(blk);
+      const int seen = blk - blk0;
+      if (a.k > 0 && seen == 2 * seen_by_bound) {
+        raise();
+        seen_by_bound = seen;
       }
-    }
-    cp_async_wait_group<kDepth - 2>();
-    const uint4 cur = ring[slot][t];
-    request(i + kDepth - 1, next);
-    slot = slot + 1 == kDepth ? 0 : slot + 1;
-    next = next + 1 == kDepth ? 0 : next + 1;
-    const float vm = vector_max<T>(cur);
-    mx = fmaxf(mx, vm);
-    if (vm > s.mu) {
-      gather();
-      if (vm < INFINITY) s.move(vm);
-      else inf = true;
-      lo = floor_of(s.mu);
+      mx = fmaxf(mx, vm);
+      if (vm > s.mu) {
+        if (vm < INFINITY) s.move(vm);
+        else inf = true;
+        lo = floor_of(s.mu);
+      }
     }
     if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0) {
-      keep = take<T>(keep_buf[w], keep, cur, tau_f, row.column(v0 + (uint32_t)i * kThreads), row.N, a.k);
-      tau_f = key_value(keep.tau);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const bool in = !(max_of<T, 1>({cur[i]}) < tau_f);
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        if (n_noted + __popc(who) > kList) {
+          keep = look<T>(keep_buf[w], keep, noted[w], n_noted, row, run0, nullptr, ~0u, a.k);
+          tau_f = key_value(keep.tau);
+          n_noted = 0;
+        }
+        if (in)
+          noted[w][n_noted + __popc(who & ((1u << lane) - 1))] = (uint32_t)((blk - blk0) * kBlock + i * kThreads + t);
+        n_noted += __popc(who);
+      }
     }
     if (fabsf(s.mu) < kFar) {
-      f2 v[kP];
-      raised<T>(cur, lo, v);
       const f2 L = pair(kLog2e, kLog2e), R = pair(-s.R, -s.R);
+      f2 S2 = 0, Y2 = 0;
 #pragma unroll
-      for (int e = 0; e < kP; ++e) {
-        const f2 y = fma2(v[e], L, R), x = ex2_2(y);
-        S2 = add2(S2, x);
-        Y2 = fma2(x, y, Y2);
+      for (int i = 0; i < kV; ++i) {
+        f2 v[kP];
+        raised<T>(cur[i], lo, v);
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+          const f2 y = fma2(v[e], L, R), x = ex2_2(y);
+          S2 = add2(S2, x);
+          Y2 = fma2(x, y, Y2);
+        }
       }
+      float x, y;
+      unpair(S2, x, y);
+      s.S += x + y;
+      unpair(Y2, x, y);
+      s.Y += x + y;
     } else {
-      const float2 r = far_sums<T>(cur, s.mu);
-      s.S += r.x;
-      s.Y += r.y;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const float2 r = far_sums<T>(cur[i], s.mu);
+        s.S += r.x;
+        s.Y += r.y;
+      }
     }
+    request(blk + kRing);
   }
   cp_async_wait_all();
-  gather();
+  uint64_t* flat = reinterpret_cast<uint64_t*>(ring);  // [kThreads], once every thread is through its blocks
+  if (a.k > 0) {
+    if (blk1 - blk0 > seen_by_bound) raise();
+    keep = look<T>(keep_buf[w], keep, noted[w], n_noted, row, run0, &ring[0][0][0],
+                   (uint32_t)max(blk1 - blk0 - kRing, 0) * kBlock, a.k);
+  }
 
   // join the threads' sums around the run's maximum
   float mu = s.mu;
@@ -687,7 +739,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
   // of the runs' bests hold any
   const uint64_t* keys = a.keys + b * n * k;
   uint64_t tau = 1;
-  if (n > k) {
+  if (n > k && n * k > kJoinThreads) {
     uint64_t head[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) head[i] = i * kJoinThreads + t < n ? keys[(int64_t)(i * kJoinThreads + t) * k] : 0;
@@ -704,10 +756,11 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
     a.top_id[b * k + rank] = (int32_t)key_id(key);
     a.top_logp[b * k + rank] = st.logp(key_value(key));
   };
-  if (c <= 256) {
+  if (c <= kJoinThreads) {  // few: each counts the keys above it
     if (t < c) {
       const uint64_t key = cand[t];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < c; ++j) rank += cand[j] > key;
       if (rank < k) emit(rank, key);
     }
@@ -831,7 +884,7 @@ inline int64_t runs(int B, int64_t blocks, int64_t ctas) {
   const int64_t n = blocks < want ? blocks : want;
   return n < 1 ? 1 : n > kMaxRuns ? kMaxRuns : n;
 }
-constexpr int kCtas = 1776, kGradCtas = 1776;
+constexpr int kCtas = 888, kGradCtas = 1776;
 
 template <typename T>
 cudaError_t launch(int B, const Args& a, cudaStream_t st) {
