@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -72,13 +73,27 @@ struct DeviceInfo {
   int sms = 0, smem_optin = 0, major = 0;
 };
 
+// Attributes of the current device, asked for once per device.
 haste_status_t device_info(DeviceInfo& di) {
   int dev = 0;
   HASTE_CUDA(cudaGetDevice(&dev));
+  constexpr int kKnown = 64;
+  static DeviceInfo known[kKnown];
+  static std::atomic<bool> is_known[kKnown];
+  if (dev >= 0 && dev < kKnown && is_known[dev].load(std::memory_order_acquire)) {
+    di = known[dev];
+    return HASTE_OK;
+  }
   HASTE_CUDA(cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev));
   HASTE_CUDA(cudaDeviceGetAttribute(&di.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
   HASTE_CUDA(cudaDeviceGetAttribute(&di.major, cudaDevAttrComputeCapabilityMajor, dev));
   if (di.major != 10) return fail(HASTE_ERR_CUDA, "libhaste needs an sm_100 GPU (found compute capability %d.x)", di.major);
+  if (dev >= 0 && dev < kKnown) {
+    static std::mutex mu;
+    std::lock_guard<std::mutex> g(mu);
+    known[dev] = di;
+    is_known[dev].store(true, std::memory_order_release);
+  }
   return HASTE_OK;
 }
 

@@ -159,7 +159,7 @@ constexpr int stages() {
 }
 template <int BN>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)stages<BN>() * (kML + BN) * kKB + 512;
+  return 1024 + (size_t)stages<BN>() * (kML + BN) * kKB + 512 + 8 * (BN / 2) * 4;
 }
 
 __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -173,6 +173,22 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_
 // Signed 8-bit operands, both K-major, 32-bit integer accumulator.
 __host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// 32 lanes x 32 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -290,51 +306,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kCols = BN / 2, CH = kCols < 16 ? kCols : 16;
+    constexpr int kCols = BN / 2, CH = kCols < 32 ? kCols : 32, kChunks = kCols / CH;
     const int q = w & 3, half = (w - 2) >> 2;
     O* out = static_cast<O*>(a.out);
+    float* sxs = reinterpret_cast<float*>(smem + (base - smem_u32(smem)) + NS * (kA + kB) + 512) + (w - 2) * kCols;
     // bf16 logits of two neighbouring labels leave as one 4-byte store when every
     // row starts on one (two 2-byte stores of a warp cover the same 64 bytes)
     const bool pairs = sizeof(O) == 2 && (a.H & 1) == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
-    int it = 0;
+    int it = 0, b_have = -1;
     for (int t = blockIdx.x; t < a.n_tiles; t += gridDim.x, ++it) {
       const int ac = it & 1;
-      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[ac], (it >> 1) & 1, abort_flag))) break;
-      tc_fence_after();
       const int h = t / a.n_bt * kML + q * 32 + lane, b0 = t % a.n_bt * BN + half * kCols;
       const float sw = h < a.H ? a.sw[h] : 0.f;
+      if (b0 != b_have) {  // this warp's copy of its samples' scales
+        __syncwarp();
+        for (int i = lane; i < kCols; i += 32) sxs[i] = a.sx[b0 + i];
+        __syncwarp();
+        b_have = b0;
+      }
+      if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[ac], (it >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
       const uint32_t src = tmem + (uint32_t)(ac * BN + half * kCols) + ((uint32_t)(q * 32) << 16);
-      for (int c = 0; c < kCols; c += CH) {
-        if (b0 + c >= a.B) break;
-        float v[CH];
-        if constexpr (CH == 16) tmem_ld16(src + (uint32_t)c, v);
-        else tmem_ld8(src + (uint32_t)c, v);
+      // the next columns leave TMEM while these are scaled and stored
+      float v[2][CH];
+      auto fetch = [&](int c, float (&to)[CH]) {
+        if constexpr (CH == 32) tmem_ld32(src + (uint32_t)(c * CH), to);
+        else if constexpr (CH == 16) tmem_ld16(src + (uint32_t)(c * CH), to);
+        else tmem_ld8(src + (uint32_t)(c * CH), to);
+      };
+      const int n_c = min(kChunks, (a.B - b0 + CH - 1) / CH);
+      const bool all = h - lane + 32 <= a.H;
+      if (n_c > 0) fetch(0, v[0]);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c >= n_c) break;
         tmem_wait_ld();
+        if (c + 1 < kChunks && c + 1 < n_c) fetch(c + 1, v[(c + 1) & 1]);
+        float(&z)[CH] = v[c & 1];
 #pragma unroll
         for (int i = 0; i < CH; i += 4) {
-          const float4 sx = *reinterpret_cast<const float4*>(a.sx + b0 + c + i);
-          v[i] = (float)__float_as_int(v[i]) * (sx.x * sw);
-          v[i + 1] = (float)__float_as_int(v[i + 1]) * (sx.y * sw);
-          v[i + 2] = (float)__float_as_int(v[i + 2]) * (sx.z * sw);
-          v[i + 3] = (float)__float_as_int(v[i + 3]) * (sx.w * sw);
+          const float4 sx = *reinterpret_cast<const float4*>(sxs + c * CH + i);
+          z[i] = (float)__float_as_int(z[i]) * (sx.x * sw);
+          z[i + 1] = (float)__float_as_int(z[i + 1]) * (sx.y * sw);
+          z[i + 2] = (float)__float_as_int(z[i + 2]) * (sx.z * sw);
+          z[i + 3] = (float)__float_as_int(z[i + 3]) * (sx.w * sw);
         }
-        O* row = out + (int64_t)(b0 + c) * a.H + h;
+        const int left = a.B - b0 - c * CH;  // samples from this column on
+        O* row = out + (int64_t)(b0 + c * CH) * a.H + h;
         if (pairs) {
-          const bool odd = lane & 1;
+          // even lanes store this label and the next for column i, odd ones the
+          // previous label and this one for column i + 1
+          const bool odd = lane & 1, in = all || h < a.H;
+          O* at = row + (odd ? (int64_t)a.H - 1 : 0);
+          const int64_t step = 2 * (int64_t)a.H;
 #pragma unroll
-          for (int i = 0; i < CH; i += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-            // even lanes store this label and the next for column i, odd ones the
-            // previous label and this one for column i + 1
-            const uint32_t pk = odd ? pack_bf16x2(got, v[i + 1]) : pack_bf16x2(v[i], got);
-            const int col = i + (odd ? 1 : 0);
-            if (h < a.H && b0 + c + col < a.B)
-              *reinterpret_cast<uint32_t*>(row + (int64_t)col * a.H - (odd ? 1 : 0)) = pk;
+          for (int i = 0; i < CH; i += 2, at += step) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? z[i] : z[i + 1], 1);
+            const uint32_t pk = odd ? pack_bf16x2(got, z[i + 1]) : pack_bf16x2(z[i], got);
+            if (in && i + (odd ? 1 : 0) < left) *reinterpret_cast<uint32_t*>(at) = pk;
           }
         } else if (h < a.H) {
 #pragma unroll
-          for (int i = 0; i < CH; ++i)
-            if (b0 + c + i < a.B) row[(int64_t)i * a.H] = Elem<O>::from_f(v[i]);
+          for (int i = 0; i < CH; ++i, row += a.H)
+            if (i < left) *row = Elem<O>::from_f(z[i]);
         }
       }
       tc_fence_before();

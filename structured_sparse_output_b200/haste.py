@@ -123,7 +123,7 @@ def _tptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream) if not hasattr(stream, "cuda_stream") else stream.cuda_stream
 
 
@@ -416,30 +416,30 @@ def haste_head_backward(Xh, Wh, dYh, dWh, dXh, ws, stream=None) -> None:
                                      _tptr(dXh), p, n, _stream(stream)), "haste_head_backward")
 
 
-def _device_of(t, name: str) -> int:
-    """The tensor's device, which must be the current one: the calls below launch there."""
+def _launch_on(dev: int, stream) -> int:
+    """The stream of a call whose tensors are on device `dev` (-1: the CPU), which must
+    be the current one: the library launches there."""
     import torch
-    if not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}; tensors must be CUDA tensors (the library reads them on the GPU)")
-    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors (the library reads them on the GPU)")
     if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
-    return dev
+        raise ValueError(f"the tensors are on cuda:{dev}, but cuda:{torch.cuda.current_device()} is current")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _ptr_on(t, name: str, dev: int) -> Optional[int]:
-    """Address of a contiguous tensor on device `dev` (None stays None)."""
-    if t is None:
-        return None
+def _arg(t, name: str, shape, dtype, dev: int) -> int:
+    """Address of a contiguous tensor of this shape and dtype on device `dev` (one
+    test on the way of every call; what failed is worked out afterwards)."""
+    if (t is not None and t.shape == shape and t.dtype == dtype and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _expect(t, name, shape, dtype)
     if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}; the call's tensors must be CUDA tensors on cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+        raise ValueError(f"{name} is on {t.device}; a call's tensors must be CUDA tensors on one device")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _ws_on(ws, dev: int):
-    return (_ptr_on(ws, "ws", dev), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
+    return (_arg(ws, "ws", ws.shape, ws.dtype, dev), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
 
 
 # ------------------------------------------------------- dense head in 8 bits
@@ -454,11 +454,11 @@ def haste_quantize_rows(x, q, scale, stream=None) -> None:
     import torch
     rows, n = x.shape
     code = dtype_code(x)
-    _expect(q, "q", (rows, (n + 15) // 16 * 16), torch.int8)
-    _expect(scale, "scale", (rows,), torch.float32)
-    dev = _device_of(x, "x")
-    _check(lib().haste_quantize_rows(rows, n, code, _ptr_on(x, "x", dev), _ptr_on(q, "q", dev),
-                                     _ptr_on(scale, "scale", dev), _stream(stream)), "haste_quantize_rows")
+    dev = x.get_device()
+    _check(lib().haste_quantize_rows(rows, n, code, _arg(x, "x", (rows, n), x.dtype, dev),
+                                     _arg(q, "q", (rows, (n + 15) // 16 * 16), torch.int8, dev),
+                                     _arg(scale, "scale", (rows,), torch.float32, dev), _launch_on(dev, stream)),
+           "haste_quantize_rows")
 
 
 def haste_head_i8_workspace_size(B: int, H: int, d: int) -> int:
@@ -472,27 +472,30 @@ def haste_head_forward_i8(Xh, Wq, w_scale, logits, ws, stream=None) -> None:
     B, d = Xh.shape
     H = Wq.shape[0]
     code, out_code = dtype_code(Xh), dtype_code(logits)
-    _expect(Wq, "Wq", (H, (d + 15) // 16 * 16), torch.int8)
-    _expect(w_scale, "w_scale", (H,), torch.float32)
-    _expect(logits, "logits", (B, H))
-    dev = _device_of(Xh, "Xh")
+    dev = Xh.get_device()
+    w = _arg(Wq, "Wq", (H, (d + 15) // 16 * 16), torch.int8, dev)
+    s = _arg(w_scale, "w_scale", (H,), torch.float32, dev)
+    out = _arg(logits, "logits", (B, H), logits.dtype, dev)
     p, n = _ws_on(ws, dev)
-    _check(lib().haste_head_forward_i8(B, H, d, code, _ptr_on(Xh, "Xh", dev), _ptr_on(Wq, "Wq", dev),
-                                       _ptr_on(w_scale, "w_scale", dev), out_code, _ptr_on(logits, "logits", dev),
-                                       p, n, _stream(stream)), "haste_head_forward_i8")
+    _check(lib().haste_head_forward_i8(B, H, d, code, _arg(Xh, "Xh", (B, d), Xh.dtype, dev), w, s, out_code, out, p, n,
+                                       _launch_on(dev, stream)), "haste_head_forward_i8")
 
 
 # ------------------------------------------------------- softmax of the logits
-def _given(row_ptr, ids, B: int, per_id, per_id_name: str) -> int:
-    """The given labels' lists (both or neither) and their fp32 values; returns nnz."""
+def _given(row_ptr, ids, per_id, per_id_name: str, B: int, dev: int):
+    """The given labels' lists (both or neither) and the address of their fp32 values:
+    (Targets, nnz, address)."""
     import torch
     if row_ptr is None:
         if ids is not None or per_id is not None:
             raise ValueError(f"ids and {per_id_name} need the given labels' row_ptr")
-        return 0
-    _targets(row_ptr, ids, B, "given")
-    _expect(per_id, per_id_name, (ids.numel(),), torch.float32)
-    return ids.numel()
+        return Targets(None, None), 0, None
+    rp = _arg(row_ptr, "given row_ptr", (B + 1,), torch.int32, dev)
+    if ids is None or ids.dim() != 1 or ids.dtype != torch.int32:
+        raise ValueError("given ids must be a 1-D int32 tensor")
+    nnz = ids.shape[0]
+    p = _arg(per_id, per_id_name, (nnz,), torch.float32, dev)
+    return Targets(rp, _arg(ids, "given ids", (nnz,), torch.int32, dev)), nnz, p
 
 
 def haste_logprob_workspace_size(B: int, N: int, dtype: int, k: int) -> int:
@@ -506,25 +509,20 @@ def haste_logprob(logits, row_ptr=None, ids=None, logp=None, lse=None, entropy=N
     alternatives top_logp and top_id [B, k]; outputs that are None are not computed."""
     import torch
     B, N = logits.shape
-    code = dtype_code(logits)
-    nnz = _given(row_ptr, ids, B, logp, "logp")
-    for n, t in (("lse", lse), ("entropy", entropy)):
-        if t is not None:
-            _expect(t, n, (B,), torch.float32)
-    k = 0
+    code, f32, dev = dtype_code(logits), torch.float32, logits.get_device()
+    given, nnz, lp = _given(row_ptr, ids, logp, "logp", B, dev)
+    ls = None if lse is None else _arg(lse, "lse", (B,), f32, dev)
+    en = None if entropy is None else _arg(entropy, "entropy", (B,), f32, dev)
+    k, tl, ti = 0, None, None
     if top_id is not None or top_logp is not None:
         if top_id is None or top_logp is None:
             raise ValueError("top_logp and top_id come together")
         k = top_id.shape[-1]
-        _expect(top_id, "top_id", (B, k), torch.int32)
-        _expect(top_logp, "top_logp", (B, k), torch.float32)
-    dev = _device_of(logits, "logits")
+        ti = _arg(top_id, "top_id", (B, k), torch.int32, dev)
+        tl = _arg(top_logp, "top_logp", (B, k), f32, dev)
     p, n = _ws_on(ws, dev)
-    given = Targets(_ptr_on(row_ptr, "row_ptr", dev), _ptr_on(ids, "ids", dev))
-    _check(lib().haste_logprob(B, N, code, _ptr_on(logits, "logits", dev), given, nnz, k, _ptr_on(logp, "logp", dev),
-                               _ptr_on(lse, "lse", dev), _ptr_on(entropy, "entropy", dev),
-                               _ptr_on(top_logp, "top_logp", dev), _ptr_on(top_id, "top_id", dev), p, n,
-                               _stream(stream)), "haste_logprob")
+    _check(lib().haste_logprob(B, N, code, _arg(logits, "logits", (B, N), logits.dtype, dev), given, nnz, k, lp, ls, en,
+                               tl, ti, p, n, _launch_on(dev, stream)), "haste_logprob")
 
 
 def haste_logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy, d_logits, stream=None) -> None:
@@ -533,16 +531,11 @@ def haste_logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy
     d_entropy may be None (no entropy term; entropy is then not read)."""
     import torch
     B, N = logits.shape
-    code = dtype_code(logits)
-    nnz = _given(row_ptr, ids, B, d_logp, "d_logp")
-    _expect(lse, "lse", (B,), torch.float32)
-    for n, t in (("entropy", entropy), ("d_entropy", d_entropy)):
-        if t is not None or (n == "entropy" and d_entropy is not None):
-            _expect(t, n, (B,), torch.float32)
-    _expect(d_logits, "d_logits", (B, N), logits.dtype)
-    dev = _device_of(logits, "logits")
-    given = Targets(_ptr_on(row_ptr, "row_ptr", dev), _ptr_on(ids, "ids", dev))
-    _check(lib().haste_logprob_backward(B, N, code, _ptr_on(logits, "logits", dev), _ptr_on(lse, "lse", dev),
-                                        _ptr_on(entropy, "entropy", dev), given, nnz, _ptr_on(d_logp, "d_logp", dev),
-                                        _ptr_on(d_entropy, "d_entropy", dev), _ptr_on(d_logits, "d_logits", dev),
-                                        _stream(stream)), "haste_logprob_backward")
+    code, f32, dev = dtype_code(logits), torch.float32, logits.get_device()
+    given, nnz, g = _given(row_ptr, ids, d_logp, "d_logp", B, dev)
+    ls = _arg(lse, "lse", (B,), f32, dev)
+    en = None if entropy is None and d_entropy is None else _arg(entropy, "entropy", (B,), f32, dev)
+    gh = None if d_entropy is None else _arg(d_entropy, "d_entropy", (B,), f32, dev)
+    out = _arg(d_logits, "d_logits", (B, N), logits.dtype, dev)
+    _check(lib().haste_logprob_backward(B, N, code, _arg(logits, "logits", (B, N), logits.dtype, dev), ls, en, given,
+                                        nnz, g, gh, out, _launch_on(dev, stream)), "haste_logprob_backward")
