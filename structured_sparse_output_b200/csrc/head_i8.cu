@@ -4,6 +4,8 @@
 // s = max|x| / 127 rounded once to fp32, q = the exact quotient x / s rounded half
 // to even.  Product: z[b, h] = (float)(sum_f qx[b, f] qw[h, f]) * (sx[b] * sw[h]),
 // the sum exact in 32 bits (tcgen05 kind::i8).
+#include <atomic>
+
 #include "common.cuh"
 
 namespace haste {
@@ -25,6 +27,34 @@ __device__ __forceinline__ int quantise(float x, float s) {
   if (r2 > s || (r2 == s && odd)) q += 1.f;
   else if (r2 < -s || (r2 == -s && odd)) q -= 1.f;
   return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// 8 of a row's elements as 8-bit integers.  x inv + 1.5 * 2^23 rounds x / s to a whole
+// number in the low bits of the sum, inv being 1 / s to an ulp; the exact remainder
+// then moves a quotient that fell on the wrong side of a half (half the row's maximum
+// lies next to 63.5, and bf16 rows meet it often).  Scales too small for a reciprocal
+// (inv = 0) take the division above.  (Divisions throughout took 249 us for 131,072
+// rows of 1,024 bf16 values, and 4 us for a single one.)
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, float inv) {
+  constexpr float kM = 12582912.f;
+  uint32_t b[8];
+  if (inv != 0.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = fmaf(x[j], inv, kM), r = fmaf(kM - t, s, x[j]), r2 = r + r;
+      b[j] = __float_as_uint(t);
+      const bool odd = b[j] & 1;
+      if (r2 > s || (r2 == s && odd)) ++b[j];
+      if (r2 < -s || (r2 == -s && odd)) --b[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = (uint32_t)quantise(x[j], s);
+  }
+  uint2 w;
+  w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return w;
 }
 
 // 8 consecutive elements of a row as fp32, 0 past its end; vec: the row starts on
@@ -58,6 +88,9 @@ constexpr int kQThreads = 256, kKeep = 4;
 template <typename T, int kWarps>
 __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict__ x, int64_t rows, int n, bool vec,
                                                              int8_t* __restrict__ q, float* __restrict__ scale) {
+  // what came before is complete before the kernel after this one may start: that
+  // one reads its weights without waiting for more
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ float red[kQThreads / 32];
   constexpr int kRowThreads = 32 * kWarps;
@@ -93,14 +126,10 @@ __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict
   }
   if (!live) return;
   const float s = m < INFINITY ? __fdiv_rn(m, 127.f) : NAN;
+  const float inv = s > 1e-30f ? __fdiv_rn(1.f, s) : 0.f;
   if (t == 0) scale[r] = s;
   auto put = [&](int i, const float (&v)[8]) {
-    uint32_t w[2] = {0, 0};
-    if (s > 0.f) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j / 4] |= (uint32_t)(quantise(v[j], s) & 0xff) << (8 * (j % 4));
-    }
-    *reinterpret_cast<uint2*>(q + r * ld + i) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(q + r * ld + i) = s > 0.f ? quantise8(v, s, inv) : make_uint2(0, 0);
   };
 #pragma unroll
   for (int c = 0; c < kKeep; ++c) {
@@ -114,16 +143,52 @@ __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict
   }
 }
 
+// A launch that may begin before the kernel before it has ended (the kernel waits
+// for that itself, griddepcontrol.wait).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Sets a kernel's attribute once per device.
+inline cudaError_t set_once(std::atomic<uint64_t>& done, const void* kern, cudaFuncAttribute attr, int value) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, attr, value);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
+
+template <typename T, int kWarps>
+cudaError_t launch_quantize_t(int64_t rows, int n, const T* x, bool vec, int8_t* q, float* scale, cudaStream_t st) {
+  constexpr int kRows = kQThreads / 32 / kWarps;
+  auto kern = k_quantize_rows<T, kWarps>;
+  // the product's split of an SM's memory, so that its CTAs can move in beside this kernel's
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = set_once(done, reinterpret_cast<const void*>(kern), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e != cudaSuccess) return e;
+  return launch_early(kern, (unsigned)((rows + kRows - 1) / kRows), kQThreads, 0, st, x, rows, n, vec, q, scale);
+}
+
 template <typename T>
 cudaError_t launch_quantize(int64_t rows, int n, const void* x, int8_t* q, float* scale, cudaStream_t st) {
   const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && n % 8 == 0;
   const T* xp = static_cast<const T*>(x);
   // a warp per row as long as its registers hold the row
-  if (n <= 256 * kKeep)
-    k_quantize_rows<T, 1><<<(unsigned)((rows + 7) / 8), kQThreads, 0, st>>>(xp, rows, n, vec, q, scale);
-  else
-    k_quantize_rows<T, 8><<<(unsigned)rows, kQThreads, 0, st>>>(xp, rows, n, vec, q, scale);
-  return cudaGetLastError();
+  return n <= 256 * kKeep ? launch_quantize_t<T, 1>(rows, n, xp, vec, q, scale, st)
+                          : launch_quantize_t<T, 8>(rows, n, xp, vec, q, scale, st);
 }
 
 // ------------------------------------------------------------- the product
@@ -407,21 +472,11 @@ cudaError_t launch_product_t(Args a, int ld, const int8_t* qx, const int8_t* qw,
   cudaError_t e = tmap_i8(&tm_w, qw, ld, a.H, kML);
   if (e == cudaSuccess) e = tmap_i8(&tm_x, qx, ld, a.B, BN);
   auto kern = k_head_i8<O, BN>;
+  static std::atomic<uint64_t> done{0};
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<BN>());
+    e = set_once(done, reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<BN>());
   if (e != cudaSuccess) return e;
-  // the launch overlaps the quantisation kernel before it (griddepcontrol.wait)
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.n_tiles < sms ? a.n_tiles : sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<BN>();
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, tm_w, tm_x);
+  return launch_early(kern, (unsigned)(a.n_tiles < sms ? a.n_tiles : sms), kThreads, smem_bytes<BN>(), st, a, tm_w, tm_x);
 }
 
 // Samples per tile: the whole batch if it fits one tile and the label tiles fill
