@@ -1,7 +1,9 @@
-"""Builds libhaste.so (sm_100a) in-tree with nvcc.
+"""Builds libhaste.so (sm_100a) in-tree with nvcc, and with g++ the Python binding's
+native argument checks, _native.so.
 
 The library is one translation unit (api.cu includes the kernel sources), linked
-against the static CUDA runtime so that it depends only on the driver.
+against the static CUDA runtime so that it depends only on the driver.  _native.so
+reads torch's tensors; it is loaded after torch, whose libraries it needs.
 """
 import os
 import subprocess
@@ -36,6 +38,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return OUT
 
 
+NATIVE_OUT = os.path.join(PKG, "_native.so")
+NATIVE_SOURCES = [os.path.join(HERE, "native.cpp"), os.path.join(HERE, "..", "..", "include", "haste.h")]
+
+
+def build_native(force: bool = False) -> str:
+    if not force and os.path.exists(NATIVE_OUT):
+        t = os.path.getmtime(NATIVE_OUT)
+        if all(os.path.getmtime(s) <= t for s in NATIVE_SOURCES):
+            return NATIVE_OUT
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = NATIVE_OUT + f".tmp{os.getpid()}"
+    subprocess.check_call(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-o", tmp, NATIVE_SOURCES[0],
+         *(a for i in include for a in ("-isystem", i)),
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L" + os.path.join(root, "lib"),
+         "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], cwd=HERE)
+    os.replace(tmp, NATIVE_OUT)
+    return NATIVE_OUT
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    build_native(force="--force" in sys.argv)
     print(OUT)

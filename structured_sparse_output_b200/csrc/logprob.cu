@@ -871,11 +871,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   }
 }
 
-// Blocks that a row of N elements can touch, wherever it starts.
+// Blocks that a row of N elements can touch: of logits at this address, or (NULL)
+// wherever they start.
 template <typename T>
-inline int64_t row_blocks(int64_t N) {
+inline int64_t row_blocks(const void* logits, int64_t N) {
   constexpr int64_t kE = 16 / sizeof(T);
-  return (N + 2 * kE - 2) / (kE * kBlock) + 1;
+  const bool on = logits && reinterpret_cast<uintptr_t>(logits) % 16 == 0 && N % kE == 0;
+  return (N + (on ? 0 : kE - 1) - 1) / (kE * kBlock) + 1;
 }
 // Runs of a row: enough CTAs for some waves, at least a block each.
 inline int64_t runs(int B, int64_t blocks, int64_t ctas) {

@@ -416,6 +416,26 @@ def haste_head_backward(Xh, Wh, dYh, dWh, dXh, ws, stream=None) -> None:
                                      _tptr(dXh), p, n, _stream(stream)), "haste_head_backward")
 
 
+_native_module = None
+
+
+def _native():
+    """The calls below with their checks made in C++ (built in-tree, like the library):
+    each returns the status, or None where a check does not hold."""
+    global _native_module
+    if _native_module is None:
+        import torch  # noqa: F401  (its libraries must be loaded first)
+        L = lib()
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise RuntimeError(f"_native.so is not built; run `python {os.path.join(_HERE, 'csrc', 'build.py')}`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.haste_logprob, L.haste_logprob_backward, L.haste_head_forward_i8)))
+        _native_module = m
+    return _native_module
+
+
 def _launch_on(dev: int, stream) -> int:
     """The stream of a call whose tensors are on device `dev` (-1: the CPU), which must
     be the current one: the library launches there."""
@@ -468,6 +488,10 @@ def haste_head_i8_workspace_size(B: int, H: int, d: int) -> int:
 def haste_head_forward_i8(Xh, Wq, w_scale, logits, ws, stream=None) -> None:
     """Head logits [B, H] (fp32 or bf16) from 8-bit weights Wq [H, haste_i8_pitch(d)]
     with a scale per label; Xh [B, d] is quantised per sample within the call."""
+    if stream is None:
+        st = (_native_module or _native()).head_forward_i8(Xh, Wq, w_scale, logits, ws)
+        if st is not None:
+            return _check(st, "haste_head_forward_i8")
     import torch
     B, d = Xh.shape
     H = Wq.shape[0]
@@ -507,6 +531,10 @@ def haste_logprob(logits, row_ptr=None, ids=None, logp=None, lse=None, entropy=N
     """Softmax reading of logits [B, N] (see include/haste.h): log p of the given
     labels (row_ptr [B + 1], ids and logp [nnz]), lse and entropy [B], and the
     alternatives top_logp and top_id [B, k]; outputs that are None are not computed."""
+    if stream is None:
+        st = (_native_module or _native()).logprob(logits, row_ptr, ids, logp, lse, entropy, top_logp, top_id, ws)
+        if st is not None:
+            return _check(st, "haste_logprob")
     import torch
     B, N = logits.shape
     code, f32, dev = dtype_code(logits), torch.float32, logits.get_device()
@@ -529,6 +557,11 @@ def haste_logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy
     """Gradient of haste_logprob's logp and entropy in the logits: d_logits [B, N] in
     their dtype.  row_ptr, ids and d_logp may be None together (no logp term), and
     d_entropy may be None (no entropy term; entropy is then not read)."""
+    if stream is None:
+        st = (_native_module or _native()).logprob_backward(logits, lse, entropy, row_ptr, ids, d_logp, d_entropy,
+                                                            d_logits)
+        if st is not None:
+            return _check(st, "haste_logprob_backward")
     import torch
     B, N = logits.shape
     code, f32, dev = dtype_code(logits), torch.float32, logits.get_device()
