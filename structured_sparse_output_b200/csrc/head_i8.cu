@@ -4,9 +4,8 @@
 // s = max|x| / 127 rounded once to fp32, q = the exact quotient x / s rounded half
 // to even.  Product: z[b, h] = (float)(sum_f qx[b, f] qw[h, f]) * (sx[b] * sw[h]),
 // the sum exact in 32 bits (tcgen05 kind::i8).
-#include <atomic>
-
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace haste {
 namespace head8 {
@@ -90,8 +89,8 @@ __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict
                                                              int8_t* __restrict__ q, float* __restrict__ scale) {
   // what came before is complete before the kernel after this one may start: that
   // one reads its weights without waiting for more
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
+  wait_for_stream();
+  let_next_start();
   __shared__ float red[kQThreads / 32];
   constexpr int kRowThreads = 32 * kWarps;
   const int64_t r = (int64_t)blockIdx.x * (kQThreads / kRowThreads) + threadIdx.x / kRowThreads;
@@ -141,34 +140,6 @@ __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict
     load8(xr, i, n, vec, v);
     put(i, v);
   }
-}
-
-// A launch that may begin before the kernel before it has ended (the kernel waits
-// for that itself, griddepcontrol.wait).
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-// Sets a kernel's attribute once per device.
-inline cudaError_t set_once(std::atomic<uint64_t>& done, const void* kern, cudaFuncAttribute attr, int value) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, attr, value);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
-  return e;
 }
 
 template <typename T, int kWarps>
@@ -325,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&full[st], kA + kB);
           tma_load_2d(SA(st), &tm_w, k * kKB, h0, &full[st]);
           if (!waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait_for_stream();
             waited = true;
           }
           tma_load_2d(SB(st), &tm_x, k * kKB, b0, &full[st]);
@@ -370,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mma_commit(done);  // also after an abort: TMEM is freed only once the MMAs end
     __syncwarp();
   } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     constexpr int kCols = BN / 2, CH = kCols < 32 ? kCols : 32, kChunks = kCols / CH;
     const int q = w & 3, half = (w - 2) >> 2;
     O* out = static_cast<O*>(a.out);

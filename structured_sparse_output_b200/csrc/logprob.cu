@@ -10,6 +10,7 @@
 #include <cfloat>
 
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace haste {
 namespace logprob {
@@ -487,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   const int n_blocks = (int)((a.N + row.head + kE * (int64_t)kBlock - 1) / (kE * (int64_t)kBlock));
   const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
   const uint32_t run0 = (uint32_t)blk0 * kBlock, v0 = run0 + t;
+  wait_for_stream();
+  let_next_start();
   // blocks [in0, in1) lie whole inside the row
   const int in0 = row.head ? 1 : 0, in1 = (int)((a.N + row.head) / (kE * (int64_t)kBlock));
   const uint4* src = reinterpret_cast<const uint4*>(row.z - row.head) + v0;
@@ -690,6 +693,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
   __shared__ int n_cand, n_best, hist[256], found[3];
   const int64_t b = blockIdx.x;
   const int t = threadIdx.x, n = a.n_run, k = a.k;
+  wait_for_stream();
+  let_next_start();
   const float4* part = a.part + b * n;
   constexpr int kPer = kMaxRuns / kJoinThreads;
   float4 p[kPer];
@@ -788,6 +793,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   const int blk0 = (int)((int64_t)run * n_blocks / a.n_run), blk1 = (int)((int64_t)(run + 1) * n_blocks / a.n_run);
   const int in0 = row.head ? 1 : 0, in1 = (int)((a.N + row.head) / (kE * (int64_t)kBlock));
   const uint4* at_row = reinterpret_cast<const uint4*>(row.z - row.head) + t;
+  wait_for_stream();
+  let_next_start();
   uint4 raw[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) raw[i] = row.load((uint32_t)blk0 * kBlock + t + i * kThreads);
@@ -890,18 +897,15 @@ constexpr int kCtas = 888, kGradCtas = 1776;
 
 template <typename T>
 cudaError_t launch(int B, const Args& a, cudaStream_t st) {
-  k_logprob<T><<<(unsigned)(B * (int64_t)a.n_run), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_logprob<T>, (unsigned)(B * (int64_t)a.n_run), kThreads, 0, st, a);
 }
 template <typename T>
 cudaError_t launch_join(int B, const Args& a, cudaStream_t st) {
-  k_logprob_join<T><<<B, kJoinThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_logprob_join<T>, (unsigned)B, kJoinThreads, 0, st, a);
 }
 template <typename T>
 cudaError_t launch_grad(int B, const GradArgs& a, cudaStream_t st) {
-  k_logprob_grad<T><<<(unsigned)(B * (int64_t)a.n_run), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_logprob_grad<T>, (unsigned)(B * (int64_t)a.n_run), kThreads, 0, st, a);
 }
 
 }  // namespace logprob
