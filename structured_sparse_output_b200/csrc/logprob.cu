@@ -25,6 +25,7 @@ constexpr int kRoom = 96;                 // and how many at most after it drops
 constexpr int kRing = 2;                  // blocks in flight or in use
 constexpr int kList = 128;                // vectors that a warp notes before it looks into them
 constexpr int kMaxRuns = 1024;            // runs of a row
+constexpr int kFew = 16;                  // alternatives for which the bound is raised less often
 
 struct Args {
   const void* logits;  // [B, N]
@@ -190,8 +191,13 @@ __device__ uint64_t kth_key(const uint64_t (&key)[kN], int k, int* hist, int* fo
     for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (key[i] != 0 && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & 255], 1);
+    for (int i = 0; i < kN; ++i) {
+      // one addition for the lanes that share a digit: most do in the first digits
+      const bool in = key[i] != 0 && (key[i] & mask) == prefix;
+      const int digit = in ? (int)(key[i] >> shift) & 255 : 256;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (in && (int)(threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
       // lane l: bins 8 (31 - l) .. + 7, so that a prefix sum counts from the top
@@ -237,19 +243,32 @@ __device__ __forceinline__ RowStats row_stats(float m, float S) {
   r.log_s = logf(S);  // NaN for a NaN or +inf in the row
   return r;
 }
+// The given labels of a row: each thread's first one is loaded early, since its logit
+// is found through two loads before it.
 template <typename T>
-__device__ __forceinline__ void write_row(const Args& a, int64_t b, const T* z, const RowStats& r, float S, float Tt) {
-  if (threadIdx.x == 0) {
-    if (a.lse) a.lse[b] = r.none ? -INFINITY : r.m + r.log_s;
-    if (a.entropy) a.entropy[b] = r.none ? 0.f : r.log_s + Tt / S;
-  }
-  int64_t p0, p1;
-  row_list(a.row_ptr, a.nnz, b, p0, p1);
-  for (int64_t p = p0 + threadIdx.x; p < p1; p += blockDim.x) {
+struct Given {
+  int64_t begin, end;
+  float z;  // of entry begin + threadIdx.x; NaN for an id outside the row
+  __device__ float logit(const Args& a, const T* row, int64_t p) const {
     const int64_t id = a.ids[p];
-    a.logp[p] = id >= 0 && id < a.N ? r.logp(Elem<T>::to_f(z[id])) : NAN;
+    return id >= 0 && id < a.N ? Elem<T>::to_f(row[id]) : NAN;
   }
-}
+  __device__ Given(const Args& a, int64_t b, const T* row) {
+    row_list(a.row_ptr, a.nnz, b, begin, end);
+    z = begin + threadIdx.x < end ? logit(a, row, begin + threadIdx.x) : 0.f;
+  }
+  // What a row gives besides its alternatives.
+  __device__ void write(const Args& a, int64_t b, const T* row, const RowStats& r, float S, float Tt) const {
+    if (threadIdx.x == 0) {
+      if (a.lse) a.lse[b] = r.none ? -INFINITY : r.m + r.log_s;
+      if (a.entropy) a.entropy[b] = r.none ? 0.f : r.log_s + Tt / S;
+    }
+    for (int64_t p = begin + threadIdx.x; p < end; p += blockDim.x) {
+      const float v = p == begin + threadIdx.x ? z : logit(a, row, p);
+      a.logp[p] = v == v ? r.logp(v) : NAN;
+    }
+  }
+};
 
 // Competing logits of one warp: the keys at or above `tau`, of which fewer than k
 // can be beaten by the others.
@@ -468,9 +487,10 @@ __device__ __noinline__ Keep look(uint64_t* buf, Keep s, const uint32_t* list, i
 // One CTA per run of a row, block by block; every thread copies its vectors of the
 // next block into its own slots of shared memory (cp.async, no barrier), which costs
 // no registers.  The threads' maxima bound the k-th best logit from below: over the
-// first block, again after 2, 4, 8 .. blocks and at the end.  A warp notes the vectors
-// whose maximum reaches the bound of the time, and looks into them at the end (or
-// when its list is full), when the bound has left few.
+// first block and again after 4, 16 .. blocks (more than 16 alternatives: after 2, 4,
+// 8 .. and at the end; raising the bound costs two barriers, about 0.4 us, and leaves
+// fewer logits to rank).  A warp notes the vectors whose maximum reaches the bound of
+// the time, and looks into them at the end (or when its list is full).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   constexpr int kE = 16 / sizeof(T), kP = kE / 2;
@@ -502,7 +522,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
         for (int i = 0; i < kV; ++i) cp_async16(smem_u32(&to[i][t]), src + i * kThreads, 16);
       } else {
 #pragma unroll 1
-        for (int i = 0; i < kV; ++i) to[i][t] = row.load(v_next + i * kThreads);
+        for (int i = 0; i < kV; ++i) {
+          const uint32_t v = v_next + i * kThreads;
+          if (row.whole(row.column(v))) cp_async16(smem_u32(&to[i][t]), src + i * kThreads, 16);
+          else to[i][t] = row.load(v);
+        }
       }
       src += kBlock;
       v_next += kBlock;
@@ -511,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   };
   request(blk0);
   request(blk0 + 1);
+  const Given<T> given(a.n_run == 1 ? a : Args{}, b, row.z);
   cp_async_wait_group<1>();
   uint4 cur[kV];
   float vm;  // of this thread's vectors of the block
@@ -522,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   };
   read(blk0);
   float mx = blk0 < blk1 ? vm : -INFINITY;  // of what this thread has seen
-  auto bound = [&] { return a.k <= 16 ? bound_of<64>(mx, a.k, group, &tau_s) : bound_of<128>(mx, a.k, group, &tau_s); };
+  auto bound = [&] { return a.k <= kFew ? bound_of<64>(mx, a.k, group, &tau_s) : bound_of<128>(mx, a.k, group, &tau_s); };
   float m = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -549,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
       cp_async_wait_group<1>();
       read(blk);
       const int seen = blk - blk0;
-      if (a.k > 0 && seen == 2 * seen_by_bound) {
+      if (a.k > 0 && seen == seen_by_bound * (a.k <= kFew ? 4 : 2)) {
         raise();
         seen_by_bound = seen;
       }
@@ -607,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   cp_async_wait_all();
   uint64_t* flat = reinterpret_cast<uint64_t*>(ring);  // [kThreads], once every thread is through its blocks
   if (a.k > 0) {
-    if (blk1 - blk0 > seen_by_bound) raise();
+    if (a.k > kFew && blk1 - blk0 > seen_by_bound) raise();
     keep = look<T>(keep_buf[w], keep, noted[w], n_noted, row, run0, &ring[0][0][0],
                    (uint32_t)max(blk1 - blk0 - kRing, 0) * kBlock, a.k);
   }
@@ -653,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   if (a.n_run > 1 && t == 0) a.part[blockIdx.x] = make_float4(mu, s.S, s.Y, 0.f);
   const float Tt = s.settle();
   const RowStats st = row_stats(mu, s.S);
-  if (a.n_run == 1) write_row(a, b, row.z, st, s.S, Tt);
+  if (a.n_run == 1) given.write(a, b, row.z, st, s.S, Tt);
   if (a.k == 0) return;
 
   uint64_t* keys = a.keys + (int64_t)blockIdx.x * a.k;
@@ -690,9 +715,13 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
   __shared__ float red[3][kJoinThreads / 32];
   __shared__ uint64_t cand[kMaxK * kMaxK];
   __shared__ uint64_t best[kMaxK];
-  __shared__ int n_cand, n_best, hist[256], found[3];
+  __shared__ int n_cand, n_best, n_lists, lists[kMaxK], hist[256], found[3];
+  __shared__ uint64_t tau_s;
   const int64_t b = blockIdx.x;
   const int t = threadIdx.x, n = a.n_run, k = a.k;
+  // the labels and the logits were complete before the runs' kernel let this one start
+  const T* row = static_cast<const T*>(a.logits) + b * a.N;
+  const Given<T> given(a, b, row);
   wait_for_stream();
   let_next_start();
   const float4* part = a.part + b * n;
@@ -707,7 +736,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
   if ((t & 31) == 0) red[0][t >> 5] = mu;
-  if (t == 0) n_cand = 0;
+  if (t == 0) n_cand = n_lists = 0;
   __syncthreads();
   for (int i = 0; i < kJoinThreads / 32; ++i) mu = fmaxf(mu, red[0][i]);
   Sums s(mu);
@@ -738,23 +767,52 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
   }
   const float Tt = s.settle();
   const RowStats st = row_stats(mu, s.S);
-  write_row(a, b, static_cast<const T*>(a.logits) + b * a.N, st, s.S, Tt);
+  given.write(a, b, row, st, s.S, Tt);
   if (k == 0) return;
-  // with more runs than alternatives, only the runs whose best is among the k best
-  // of the runs' bests hold any
+  // A bound that few keys beside the k best reach.  Up to k runs: the smallest of the
+  // runs' ceil(k / n)-th bests, since k keys are as large.  More: the k-th largest of
+  // the runs' bests, below which a run holds nothing.
   const uint64_t* keys = a.keys + b * n * k;
   uint64_t tau = 1;
+  int m = n;  // runs that are looked into
   if (n > k && n * k > kJoinThreads) {
     uint64_t head[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) head[i] = i * kJoinThreads + t < n ? keys[(int64_t)(i * kJoinThreads + t) * k] : 0;
     tau = kth_key(head, k, hist, found);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (head[i] != 0 && head[i] >= tau) lists[atomicAdd(&n_lists, 1)] = i * kJoinThreads + t;
+    m = k;
     __syncthreads();
+  } else if (n <= k) {
+    if (t < 32) {
+      uint64_t low = ~0ull;
+      for (int i = t; i < n; i += 32) {
+        const uint64_t key = keys[(int64_t)i * k + (k + n - 1) / n - 1];
+        low = key < low ? key : low;  // 0 where a short run ends before
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, low, o);
+        low = other < low ? other : low;
+      }
+      if (t == 0) tau_s = low;
+    }
+    __syncthreads();
+    tau = tau_s > 0 ? tau_s : 1;
   }
-  for (int i = t; i < n * k; i += kJoinThreads) {
-    const uint64_t key = keys[i];
-    if (key != 0 && key >= tau) cand[atomicAdd(&n_cand, 1)] = key;
+  constexpr int kPerCand = kMaxK * kMaxK / kJoinThreads;
+  uint64_t got[kPerCand];
+#pragma unroll
+  for (int i = 0; i < kPerCand; ++i) {
+    const int at = i * kJoinThreads + t;
+    got[i] = 0;
+    if (at < m * k) got[i] = keys[(int64_t)(m < n ? lists[at / k] : at / k) * k + at % k];
   }
+#pragma unroll
+  for (int i = 0; i < kPerCand; ++i)
+    if (got[i] != 0 && got[i] >= tau) cand[atomicAdd(&n_cand, 1)] = got[i];
   __syncthreads();
   const int c = n_cand;
   auto emit = [&](int rank, uint64_t key) {
@@ -770,11 +828,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) k_logprob_join(Args a) {
       if (rank < k) emit(rank, key);
     }
   } else {
-    uint64_t key[kMaxK * kMaxK / kJoinThreads];
-#pragma unroll
-    for (int i = 0; i < kMaxK * kMaxK / kJoinThreads; ++i)
-      key[i] = i * kJoinThreads + t < c ? cand[i * kJoinThreads + t] : 0;
-    emit_best(key, k, hist, found, best, &n_best, emit);
+    emit_best(got, k, hist, found, best, &n_best, emit);
   }
 }
 
@@ -886,14 +940,22 @@ inline int64_t row_blocks(const void* logits, int64_t N) {
   const bool on = logits && reinterpret_cast<uintptr_t>(logits) % 16 == 0 && N % kE == 0;
   return (N + (on ? 0 : kE - 1) - 1) / (kE * kBlock) + 1;
 }
-// Runs of a row: enough CTAs for some waves, at least a block each.
-inline int64_t runs(int B, int64_t blocks, int64_t ctas) {
-  if (B >= 128 && blocks <= 4) return 1;
+// Runs of a row: `ctas` CTAs in all, at least `least` blocks each.
+inline int64_t runs(int B, int64_t blocks, int64_t ctas, int64_t least) {
   const int64_t want = (ctas + B - 1) / B;
-  const int64_t n = blocks < want ? blocks : want;
+  const int64_t n = blocks / least < want ? blocks / least : want;
   return n < 1 ? 1 : n > kMaxRuns ? kMaxRuns : n;
 }
-constexpr int kCtas = 888, kGradCtas = 1776;
+// Whole rows where that leaves the SMs busy or a row is short: the start of a run
+// and the join cost as much as several blocks.  Measured with 5 alternatives, whole
+// against split: 256 x 65,536 bf16 13.1 and 20.4 us, 256 x 131,072 20.1 and 25.2 us,
+// 64 x 32,003 8.7 and 9.4 us; but 1 x 65,536 9.6 and 6.9 us, 256 x 670,208 (4 runs)
+// 87 and 73 us.
+inline int64_t forward_runs(int B, int64_t blocks) {
+  if (blocks <= 4 || (B >= 64 && blocks <= 8) || (B >= 128 && blocks <= 16)) return 1;
+  return runs(B, blocks, 888, 2);
+}
+inline int64_t grad_runs(int B, int64_t blocks) { return runs(B, blocks, 1776, 1); }
 
 template <typename T>
 cudaError_t launch(int B, const Args& a, cudaStream_t st) {
