@@ -80,10 +80,30 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int i, int n, b
   }
 }
 
+// The largest magnitude so far; a NaN counts as infinite.
+__device__ __forceinline__ float row_max(float m, const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a = fabsf(v[j]);
+    m = a <= m ? m : a < INFINITY ? a : INFINITY;
+  }
+  return m;
+}
+// A row's scale, from its largest magnitude (infinite: NaN, and every q = 0).
+struct RowScale {
+  float s, inv;
+  __device__ explicit RowScale(float m) {
+    s = m < INFINITY ? __fdiv_rn(m, 127.f) : NAN;
+    inv = s > 1e-30f ? __fdiv_rn(1.f, s) : 0.f;
+  }
+  __device__ uint2 quantised(const float (&v)[8]) const { return s > 0.f ? quantise8(v, s, inv) : make_uint2(0, 0); }
+};
+
 // One row per group of kWarps warps; every lane holds kKeep runs of 8 elements of
 // its row (rows of up to 256 kWarps kKeep elements are read once), longer rows are
 // read again from L2.  A row with a NaN or an infinity gets the scale NaN and zeros.
 constexpr int kQThreads = 256, kKeep = 4;
+constexpr int64_t kManyRows = 4096;
 template <typename T, int kWarps>
 __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict__ x, int64_t rows, int n, bool vec,
                                                              int8_t* __restrict__ q, float* __restrict__ scale) {
@@ -100,21 +120,16 @@ __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict
   const T* xr = x + (live ? r : 0) * n;
   float keep[kKeep][8];
   float m = 0.f;
-  auto take = [&](const float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(v[j]);
-      m = a <= m ? m : a < INFINITY ? a : INFINITY;  // NaN counts as infinite
-    }
-  };
+  for (int c = 0; c < kKeep; ++c)
+    if (c * kRowThreads * 8 < n) load8(xr, (c * kRowThreads + t) * 8, n, vec, keep[c]);
 #pragma unroll
-  for (int c = 0; c < kKeep; ++c) load8(xr, (c * kRowThreads + t) * 8, n, vec, keep[c]);
-#pragma unroll
-  for (int c = 0; c < kKeep; ++c) take(keep[c]);
+  for (int c = 0; c < kKeep; ++c)
+    if (c * kRowThreads * 8 < n) m = row_max(m, keep[c]);
   for (int i = (kKeep * kRowThreads + t) * 8; i < n; i += kRowThreads * 8) {
     float v[8];
     load8(xr, i, n, vec, v);
-    take(v);
+    m = row_max(m, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -124,12 +139,9 @@ __global__ void __launch_bounds__(kQThreads) k_quantize_rows(const T* __restrict
     for (int i = 0; i < kWarps; ++i) m = fmaxf(m, red[threadIdx.x / kRowThreads * kWarps + i]);
   }
   if (!live) return;
-  const float s = m < INFINITY ? __fdiv_rn(m, 127.f) : NAN;
-  const float inv = s > 1e-30f ? __fdiv_rn(1.f, s) : 0.f;
-  if (t == 0) scale[r] = s;
-  auto put = [&](int i, const float (&v)[8]) {
-    *reinterpret_cast<uint2*>(q + r * ld + i) = s > 0.f ? quantise8(v, s, inv) : make_uint2(0, 0);
-  };
+  const RowScale s(m);
+  if (t == 0) scale[r] = s.s;
+  auto put = [&](int i, const float (&v)[8]) { *reinterpret_cast<uint2*>(q + r * ld + i) = s.quantised(v); };
 #pragma unroll
   for (int c = 0; c < kKeep; ++c) {
     const int i = (c * kRowThreads + t) * 8;
@@ -157,9 +169,11 @@ template <typename T>
 cudaError_t launch_quantize(int64_t rows, int n, const void* x, int8_t* q, float* scale, cudaStream_t st) {
   const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && n % 8 == 0;
   const T* xp = static_cast<const T*>(x);
-  // a warp per row as long as its registers hold the row
-  return n <= 256 * kKeep ? launch_quantize_t<T, 1>(rows, n, xp, vec, q, scale, st)
-                          : launch_quantize_t<T, 8>(rows, n, xp, vec, q, scale, st);
+  // a warp per row where its registers hold the row and the rows fill the SMs; more
+  // warps, which end sooner, for the rows of a batch (one row of 768: 2.2 and 1.6 us)
+  if (n <= 256 * kKeep && rows >= kManyRows) return launch_quantize_t<T, 1>(rows, n, xp, vec, q, scale, st);
+  if (n <= 2 * 256 * kKeep) return launch_quantize_t<T, 4>(rows, n, xp, vec, q, scale, st);
+  return launch_quantize_t<T, 8>(rows, n, xp, vec, q, scale, st);
 }
 
 // ------------------------------------------------------------- the product
@@ -178,7 +192,7 @@ constexpr int kKB = 128;      // K bytes per stage
 constexpr int kMaxStages = 8;
 constexpr int kMaxBH = 1 << 30;  // B and H: tile coordinates are 32-bit
 // Tiles of the narrowest form a batch of B can take.
-inline int64_t max_tiles(int64_t B, int64_t H) { return (H + kML - 1) / kML * (B <= 64 ? 1 : (B + 63) / 64); }
+inline int64_t max_tiles(int64_t B, int64_t H) { return (H + kML - 1) / kML * ((B + 15) / 16); }
 
 struct Args {
   int B, H, nk;  // nk: K stages of a tile
@@ -236,6 +250,70 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   return true;
 }
 
+// One warp's share of a finished tile: kCols samples from b0 on of the 32 labels of
+// its TMEM lane quarter (this lane's label is h), scaled and stored.  The next columns
+// leave TMEM while these are stored.
+template <typename O, int kCols>
+__device__ __forceinline__ void store_tile(const Args& a, uint32_t src, int h, int b0, const float* sxs) {
+  constexpr int CH = kCols < 32 ? kCols : 32, kChunks = kCols / CH;
+  const int lane = threadIdx.x & 31;
+  O* out = static_cast<O*>(a.out);
+  const float sw = h < a.H ? a.sw[h] : 0.f;
+  // bf16 logits of two neighbouring labels leave as one 4-byte store when every row
+  // starts on one (two 2-byte stores of a warp cover the same 64 bytes)
+  const bool pairs = sizeof(O) == 2 && (a.H & 1) == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
+  const bool all = h - lane + 32 <= a.H;
+  const int n_c = min(kChunks, (a.B - b0 + CH - 1) / CH);
+  float v[2][CH];
+  auto fetch = [&](int c, float (&to)[CH]) {
+    if constexpr (CH == 32) tmem_ld32(src + (uint32_t)(c * CH), to);
+    else if constexpr (CH == 16) tmem_ld16(src + (uint32_t)(c * CH), to);
+    else tmem_ld8(src + (uint32_t)(c * CH), to);
+  };
+  if (n_c > 0) fetch(0, v[0]);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    if (c >= n_c) break;
+    tmem_wait_ld();
+    if (c + 1 < kChunks && c + 1 < n_c) fetch(c + 1, v[(c + 1) & 1]);
+    float(&z)[CH] = v[c & 1];
+#pragma unroll
+    for (int i = 0; i < CH; i += 4) {
+      const float4 sx = *reinterpret_cast<const float4*>(sxs + c * CH + i);
+      z[i] = (float)__float_as_int(z[i]) * (sx.x * sw);
+      z[i + 1] = (float)__float_as_int(z[i + 1]) * (sx.y * sw);
+      z[i + 2] = (float)__float_as_int(z[i + 2]) * (sx.z * sw);
+      z[i + 3] = (float)__float_as_int(z[i + 3]) * (sx.w * sw);
+    }
+    const int left = a.B - b0 - c * CH;  // samples from this column on
+    O* row = out + (int64_t)(b0 + c * CH) * a.H + h;
+    if (pairs) {
+      // even lanes store this label and the next for column i, odd ones the previous
+      // label and this one for column i + 1
+      const bool odd = lane & 1, in = all || h < a.H;
+      O* at = row + (odd ? (int64_t)a.H - 1 : 0);
+      const int64_t step = 2 * (int64_t)a.H;
+#pragma unroll
+      for (int i = 0; i < CH; i += 2, at += step) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? z[i] : z[i + 1], 1);
+        const uint32_t pk = odd ? pack_bf16x2(got, z[i + 1]) : pack_bf16x2(z[i], got);
+        if (in && i + (odd ? 1 : 0) < left) *reinterpret_cast<uint32_t*>(at) = pk;
+      }
+    } else if (h < a.H) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i, row += a.H)
+        if (i < left) *row = Elem<O>::from_f(z[i]);
+    }
+  }
+}
+
+// A warp's copy of its samples' scales.
+__device__ __forceinline__ void copy_scales(float* sxs, const float* sx, int n) {
+  __syncwarp();
+  for (int i = threadIdx.x & 31; i < n; i += 32) sxs[i] = sx[i];
+  __syncwarp();
+}
+
 template <typename O, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_head_i8(Args a, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {
@@ -257,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_w) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_x) : "memory");
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -277,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  let_next_start();
 
   if (w == 0) {
     if (lane == 0) {
@@ -342,71 +423,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     wait_for_stream();
-    constexpr int kCols = BN / 2, CH = kCols < 32 ? kCols : 32, kChunks = kCols / CH;
+    constexpr int kCols = BN / 2;
     const int q = w & 3, half = (w - 2) >> 2;
-    O* out = static_cast<O*>(a.out);
     float* sxs = reinterpret_cast<float*>(smem + (base - smem_u32(smem)) + NS * (kA + kB) + 512) + (w - 2) * kCols;
-    // bf16 logits of two neighbouring labels leave as one 4-byte store when every
-    // row starts on one (two 2-byte stores of a warp cover the same 64 bytes)
-    const bool pairs = sizeof(O) == 2 && (a.H & 1) == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
     int it = 0, b_have = -1;
     for (int t = blockIdx.x; t < a.n_tiles; t += gridDim.x, ++it) {
       const int ac = it & 1;
       const int h = t / a.n_bt * kML + q * 32 + lane, b0 = t % a.n_bt * BN + half * kCols;
-      const float sw = h < a.H ? a.sw[h] : 0.f;
-      if (b0 != b_have) {  // this warp's copy of its samples' scales
-        __syncwarp();
-        for (int i = lane; i < kCols; i += 32) sxs[i] = a.sx[b0 + i];
-        __syncwarp();
+      if (b0 != b_have) {
+        copy_scales(sxs, a.sx + b0, kCols);
         b_have = b0;
       }
       if (!__all_sync(0xffffffffu, wait_or_abort(&acc_full[ac], (it >> 1) & 1, abort_flag))) break;
       tc_fence_after();
-      const uint32_t src = tmem + (uint32_t)(ac * BN + half * kCols) + ((uint32_t)(q * 32) << 16);
-      // the next columns leave TMEM while these are scaled and stored
-      float v[2][CH];
-      auto fetch = [&](int c, float (&to)[CH]) {
-        if constexpr (CH == 32) tmem_ld32(src + (uint32_t)(c * CH), to);
-        else if constexpr (CH == 16) tmem_ld16(src + (uint32_t)(c * CH), to);
-        else tmem_ld8(src + (uint32_t)(c * CH), to);
-      };
-      const int n_c = min(kChunks, (a.B - b0 + CH - 1) / CH);
-      const bool all = h - lane + 32 <= a.H;
-      if (n_c > 0) fetch(0, v[0]);
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (c >= n_c) break;
-        tmem_wait_ld();
-        if (c + 1 < kChunks && c + 1 < n_c) fetch(c + 1, v[(c + 1) & 1]);
-        float(&z)[CH] = v[c & 1];
-#pragma unroll
-        for (int i = 0; i < CH; i += 4) {
-          const float4 sx = *reinterpret_cast<const float4*>(sxs + c * CH + i);
-          z[i] = (float)__float_as_int(z[i]) * (sx.x * sw);
-          z[i + 1] = (float)__float_as_int(z[i + 1]) * (sx.y * sw);
-          z[i + 2] = (float)__float_as_int(z[i + 2]) * (sx.z * sw);
-          z[i + 3] = (float)__float_as_int(z[i + 3]) * (sx.w * sw);
-        }
-        const int left = a.B - b0 - c * CH;  // samples from this column on
-        O* row = out + (int64_t)(b0 + c * CH) * a.H + h;
-        if (pairs) {
-          // even lanes store this label and the next for column i, odd ones the
-          // previous label and this one for column i + 1
-          const bool odd = lane & 1, in = all || h < a.H;
-          O* at = row + (odd ? (int64_t)a.H - 1 : 0);
-          const int64_t step = 2 * (int64_t)a.H;
-#pragma unroll
-          for (int i = 0; i < CH; i += 2, at += step) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? z[i] : z[i + 1], 1);
-            const uint32_t pk = odd ? pack_bf16x2(got, z[i + 1]) : pack_bf16x2(z[i], got);
-            if (in && i + (odd ? 1 : 0) < left) *reinterpret_cast<uint32_t*>(at) = pk;
-          }
-        } else if (h < a.H) {
-#pragma unroll
-          for (int i = 0; i < CH; ++i, row += a.H)
-            if (i < left) *row = Elem<O>::from_f(z[i]);
-        }
-      }
+      store_tile<O, kCols>(a, tmem + (uint32_t)(ac * BN + half * kCols) + ((uint32_t)(q * 32) << 16), h, b0, sxs);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ac]);
@@ -450,8 +480,25 @@ cudaError_t launch_product_t(Args a, int ld, const int8_t* qx, const int8_t* qw,
   return launch_early(kern, (unsigned)(a.n_tiles < sms ? a.n_tiles : sms), kThreads, smem_bytes<BN>(), st, a, tm_w, tm_x);
 }
 
-// Samples per tile: the whole batch if it fits one tile and the label tiles fill
-// the SMs; narrower tiles otherwise, down to 64.
+// Samples per tile: the width (not above the batch's, rounded up) whose rounds of tiles
+// over the SMs stage the fewest bytes, 128 + BN rows a tile.  Measured against the
+// others at d = 768: 256 x 16,384 labels 10.6 us with 256 (12.1 with 128, 16.0 with
+// 64), 256 x 8,192 8.4 us with 128 (10.3 with 64).
+inline int tile_samples(int B, int H, int sms) {
+  const int64_t lt = (H + kML - 1) / kML;
+  int best = 16;
+  int64_t least = INT64_MAX;
+  for (int bn = 16; bn <= 256; bn *= 2) {
+    const int64_t rounds = (lt * ((B + bn - 1) / bn) + sms - 1) / sms, rows = rounds * (kML + bn);
+    if (rows <= least) {
+      best = bn;
+      least = rows;
+    }
+    if (bn >= B) break;
+  }
+  return best;
+}
+
 template <typename O>
 cudaError_t launch_product(int B, int H, int ld, const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,
                            void* out, int sms, cudaStream_t st) {
@@ -462,10 +509,7 @@ cudaError_t launch_product(int B, int H, int ld, const int8_t* qx, const float* 
   a.sx = sx;
   a.sw = sw;
   a.out = out;
-  const int64_t lt = (H + kML - 1) / kML;
-  int bn = B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : 256;
-  while (bn > 64 && lt * ((B + bn - 1) / bn) < sms) bn /= 2;
-  switch (bn) {
+  switch (tile_samples(B, H, sms)) {
     case 16: return launch_product_t<O, 16>(a, ld, qx, qw, sms, st);
     case 32: return launch_product_t<O, 32>(a, ld, qx, qw, sms, st);
     case 64: return launch_product_t<O, 64>(a, ld, qx, qw, sms, st);
