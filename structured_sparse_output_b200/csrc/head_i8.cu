@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[s], 8);
     }
     mbar_init(done, 1);
-    *abort_flag = 0;
+    // a limit shorter than one sleep: every warp's first wait runs out at once
+    *abort_flag = g_wait_limit_ns < kWaitSuspendNs;
+    if (*abort_flag) record_error(kErrTimeout);
     fence_mbar_init();
   }
   if (w == 1) {

@@ -858,10 +858,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   int64_t p0, p1;
   row_list(a.row_ptr, a.nnz, b, p0, p1);
   float G = 0.f;  // every warp sums the list in the same order
+  bool ascending = true;
   for (int64_t p = p0 + (t & 31); p < p1; p += 32) {
     const int64_t id = a.ids[p];
     if (id >= 0 && id < a.N) G += a.d_logp[p];
+    ascending &= p + 1 == p1 || id < a.ids[p + 1];
   }
+  ascending = __all_sync(0xffffffffu, ascending);  // then no label is given twice
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
   // the definition, for single labels and where R would lose too much
@@ -921,9 +924,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   for (int64_t p = p0 + t; p < p1; p += kThreads) {
     const int64_t id = a.ids[p];
     if (id < 0 || id >= a.N || id < c0 || id >= c1) continue;
-    float g = 0.f;
+    float g = ascending ? a.d_logp[p] : 0.f;
     bool first = true;
-    for (int64_t q = p0; q < p1; ++q)
+    for (int64_t q = p0; q < p1 && !ascending; ++q)
       if (a.ids[q] == id) {
         if (q < p) first = false;
         g += a.d_logp[q];

@@ -193,6 +193,46 @@ def test_streams_graphs_and_shared_workspace():
         _check(o2, x2.double().cpu().numpy(), q, s, "f32")
 
 
+def test_short_wait_limit_unwinds_and_the_context_survives():
+    """A 1 ns limit on the product's inter-warp waits: the kernel unwinds and the error
+    word says so; with the default restored the same call is right."""
+    rng = np.random.default_rng(4)
+    q, s = _quantize(_at(rng.standard_normal((3000, 800)), "f32")[0])
+    xt, x64 = _at(rng.standard_normal((200, 800)), "bf16")
+    torch.cuda.synchronize()
+    assert H.haste_device_status() == H.HASTE_OK
+    H.haste_set_wait_limit_ns(1)
+    try:
+        _head(xt, q, s, "f32")
+        assert H.haste_device_status() == H.HASTE_ERR_TIMEOUT
+    finally:
+        H.haste_set_wait_limit_ns(0)
+    assert H.haste_device_status() == H.HASTE_OK
+    out, _ = _head(xt, q, s, "f32")
+    _check(out, x64, q, s, "f32")
+
+
+def test_binding_refuses_what_the_calls_cannot_read():
+    x, q, s = torch.zeros(3, 40, device="cuda"), torch.zeros(5, 48, dtype=torch.int8, device="cuda"), torch.ones(5, device="cuda")
+    out, ws = torch.zeros(3, 5, device="cuda"), torch.empty(4096, dtype=torch.uint8, device="cuda")
+    H.haste_head_forward_i8(x, q, s, out, ws)
+    for call, what in [(lambda: H.haste_head_forward_i8(x.t().contiguous().t(), q, s, out, ws), "contiguous"),
+                       (lambda: H.haste_head_forward_i8(x, q[:, :40], s, out, ws), "shape"),
+                       (lambda: H.haste_head_forward_i8(x, q, s, out[:, :4], ws), "shape"),
+                       (lambda: H.haste_head_forward_i8(x, q, s.cpu(), out, ws), "w_scale"),
+                       (lambda: H.haste_quantize_rows(x, q, s), "shape")]:
+        with pytest.raises(ValueError, match=what):
+            call()
+    for w, status in [(None, H.HASTE_ERR_WORKSPACE), (ws[:64], H.HASTE_ERR_WORKSPACE), (ws[1:], H.HASTE_ERR_INVALID_ARG)]:
+        with pytest.raises(H.HasteError) as e:
+            H.haste_head_forward_i8(x, q, s, out, w)
+        assert e.value.status == status
+    off = torch.zeros(5 * 48 + 8, dtype=torch.int8, device="cuda")[8:].view(5, 48)
+    with pytest.raises(H.HasteError) as e:
+        H.haste_head_forward_i8(x, off, s, out, ws)                               # rows must start on 16 bytes
+    assert e.value.status == H.HASTE_ERR_INVALID_ARG
+
+
 def test_scoring_run_quantise_product_alternatives():
     """Weights quantised once, 8-bit logits, log probabilities with the best labels: the
     whole run against fp64.  The logits are the same fp32 numbers on both sides (an

@@ -252,8 +252,9 @@ def test_gradient_patterns(N, dt):
 
 def test_gradient_long_list_and_no_terms():
     rng = np.random.default_rng(8)
-    zt, z = _logits(rng.standard_normal((2, 3000)), "f32")
+    zt, z = _logits(rng.standard_normal((3, 3000)), "f32")
     rp, ids = _lists([2500, 1], 3000, rng, messy=True)
+    rp, ids = np.concatenate([rp, [rp[-1] + 3000]]).astype(np.int32), np.concatenate([ids, np.arange(3000, dtype=np.int32)])
     g = rng.standard_normal(len(ids)).astype(np.float32)
     _, lse, ent, _, _ = _run(zt, rp, ids, 0)
     dz = torch.empty_like(zt)
@@ -318,6 +319,84 @@ def test_on_another_stream_and_captured():
         torch.cuda.synchronize()
         _check(o, z, rp, ids, 7)
         _check_grad(to_np64(dz), z, rp, ids, np.ones(12, np.float32), None, "bf16")
+
+
+def test_two_calls_at_once_on_two_streams_and_in_one_graph():
+    """Calls on two streams with a workspace each, eagerly and captured as a fork that
+    joins; then two graphs that share one workspace, replayed in turn."""
+    rng = np.random.default_rng(12)
+    B, N, k = 3, 300_000, 9
+    zs = [_logits(rng.standard_normal((B, N)) * (i + 1), "bf16") for i in range(2)]
+    outs = [[None, torch.empty(B, device="cuda"), torch.empty(B, device="cuda"), torch.empty(B, k, device="cuda"),
+             torch.empty(B, k, dtype=torch.int32, device="cuda")] for _ in range(2)]
+    size = H.haste_logprob_workspace_size(B, N, H.HASTE_BF16, k)
+    assert size > 0
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    none = np.zeros(B + 1, np.int32)
+
+    def call(i, w):
+        H.haste_logprob(zs[i][0], lse=outs[i][1], entropy=outs[i][2], top_logp=outs[i][3], top_id=outs[i][4], ws=w)
+
+    def check():
+        torch.cuda.synchronize()
+        for i in range(2):
+            _check([torch.empty(0)] + outs[i][1:], zs[i][1], none, np.zeros(0, np.int32), k)
+            for t in outs[i][1:]:
+                t.fill_(-3)
+        torch.cuda.synchronize()
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def fork():
+        side.wait_stream(main)
+        call(0, ws[0])
+        with torch.cuda.stream(side):
+            call(1, ws[1])
+        main.wait_stream(side)
+
+    with torch.cuda.stream(main):
+        for _ in range(5):
+            fork()
+    check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        fork()
+        fork()
+    g.replay()
+    check()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            call(i, ws[0])
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+    check()
+
+
+def test_non_contiguous_and_mixed_tensors_are_refused():
+    z = torch.zeros(4, 64, device="cuda")
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    for call, what in [(lambda: H.haste_logprob(z[:, ::2], lse=f(4)), "contiguous"),
+                       (lambda: H.haste_logprob(z.t(), lse=f(64)), "contiguous"),
+                       (lambda: H.haste_logprob(z, lse=f(8)[::2]), "contiguous"),
+                       (lambda: H.haste_logprob(z, lse=torch.zeros(4)), "lse"),
+                       (lambda: H.haste_logprob(z, lse=f(5)), "shape"),
+                       (lambda: H.haste_logprob_backward(z, f(4), None, None, None, None, None, f(64, 4).t()), "contiguous")]:
+        with pytest.raises(ValueError, match=what):
+            call()
+    with pytest.raises(H.HasteError) as e:
+        H.haste_logprob_backward(z, f(4), None, None, None, None, None, z)      # in place
+    assert e.value.status == H.HASTE_ERR_INVALID_ARG
+    k = torch.zeros(4, 65, dtype=torch.int32, device="cuda")
+    with pytest.raises(H.HasteError) as e:
+        H.haste_logprob(z, top_logp=f(4, 65), top_id=k)
+    assert e.value.status == H.HASTE_ERR_INVALID_ARG
+    long = torch.zeros(2, 400_000, device="cuda")
+    with pytest.raises(H.HasteError) as e:
+        H.haste_logprob(long, lse=f(2))                                          # split rows need a workspace
+    assert e.value.status == H.HASTE_ERR_WORKSPACE
 
 
 def test_softmax_training_step_of_the_head():
