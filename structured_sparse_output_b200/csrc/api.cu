@@ -1190,8 +1190,19 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void*
   DeviceInfo di;
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  logprob::Args a{logits, N,       nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, k, n_run, logp, lse,
-                  entropy, top_logp, top_id};
+  logprob::Args a{};
+  a.logits = logits;
+  a.N = N;
+  a.row_ptr = nnz > 0 ? given.row_ptr : nullptr;
+  a.ids = given.ids;
+  a.nnz = nnz;
+  a.k = k;
+  a.n_run = n_run;
+  a.logp = logp;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_logp = top_logp;
+  a.top_id = top_id;
   if (n_run > 1) {
     a.part = static_cast<float4*>(ws);
     a.keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(ws) + keys);

@@ -35,6 +35,9 @@ struct Args {
   int64_t nnz;
   int k;
   int n_run;  // runs that a row is split into, one CTA each
+  // Rows too short to give k groups of threads a logit: the bound takes groups of one
+  // thread, or (a few hundred logits) every logit is ranked without one.
+  int thin, rank_all;
   float* logp;
   float* lse;
   float* entropy;
@@ -343,14 +346,14 @@ __device__ __noinline__ Keep take(uint64_t* buf, Keep s, uint4 raw, bool live, i
 
 // A lower bound of the k-th best of what the block's threads have seen, from their
 // maxima: the k-th largest of the maxima of kG groups of threads (k <= kG), as a
-// rank value without its low 7 bits, which tell equal maxima apart.
+// rank value without its low 8 bits, which tell equal maxima apart.
 template <int kG>
-__device__ uint32_t bound_of(float mx, int k, uint32_t* group, uint32_t* out) {
+__device__ __forceinline__ uint32_t bound_of(float mx, int k, uint32_t* group, uint32_t* out) {
   constexpr int kL = kThreads / kG, kPart = kG / kL;  // lanes of a group, groups that a lane compares with
   const int t = threadIdx.x;
 #pragma unroll
   for (int o = 1; o < kL; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const uint32_t mine = (rank_value(mx) & ~127u) | (uint32_t)(t / kL);
+  const uint32_t mine = (rank_value(mx) & ~255u) | (uint32_t)(t / kL);
   if (t % kL == 0) group[t / kL] = mine;
   __syncthreads();
   int above = 0;
@@ -361,7 +364,26 @@ __device__ uint32_t bound_of(float mx, int k, uint32_t* group, uint32_t* out) {
   }
 #pragma unroll
   for (int o = 1; o < kL; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
-  if (above == k - 1 && t % kL == 0) *out = mine & ~127u;
+  if (above == k - 1 && t % kL == 0) *out = mine & ~255u;
+  __syncthreads();
+  return *out;
+}
+
+// The same for a row that only the first 128 threads hold a vector of: groups of one.
+__device__ __noinline__ uint32_t bound_thin(float mx, int k, uint32_t* group, uint32_t* out) {
+  const int t = threadIdx.x;
+  const uint32_t mine = (rank_value(mx) & ~255u) | (uint32_t)(t & 127);
+  if (t < 128) group[t] = mine;
+  __syncthreads();
+  if (t < 128) {
+    int above = 0;
+#pragma unroll 8
+    for (int i = 0; i < 128; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&group[i]);
+      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    }
+    if (above == k - 1) *out = mine & ~255u;
+  }
   __syncthreads();
   return *out;
 }
@@ -547,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   };
   read(blk0);
   float mx = blk0 < blk1 ? vm : -INFINITY;  // of what this thread has seen
-  auto bound = [&] { return a.k <= kFew ? bound_of<64>(mx, a.k, group, &tau_s) : bound_of<128>(mx, a.k, group, &tau_s); };
+  if (a.rank_all)
+    for (uint32_t j = t; j < row.N; j += kThreads) keep_buf[0][j] = rank_key(Elem<T>::to_f(row.z[j]), j);
   float m = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -555,18 +578,24 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   Keep keep{0, 0};
   float tau_f = INFINITY;
   auto raise = [&] {
-    const uint64_t up = (uint64_t)bound() << 32;
+    const uint64_t up = (uint64_t)(a.k <= kFew ? bound_of<64>(mx, a.k, group, &tau_s)
+                                               : bound_of<128>(mx, a.k, group, &tau_s)) << 32;
     if (up > keep.tau) keep.tau = up;
     tau_f = key_value(keep.tau);
   };
-  if (a.k > 0) raise();
-  else __syncthreads();
-  int n_noted = 0, seen_by_bound = 1;
+  if (a.k == 0 || a.rank_all) {
+    __syncthreads();
+  } else if (a.thin) {
+    keep.tau = (uint64_t)bound_thin(mx, a.k, group, &tau_s) << 32;
+    tau_f = key_value(keep.tau);
+  } else {
+    raise();
+  }
+  int n_noted = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) m = fmaxf(m, red[0][i]);
   Sums s(m < INFINITY ? fmaxf(m, -FLT_MAX) : 0.f);
-  float lo = floor_of(s.mu);
-  bool inf = !(m < INFINITY);
+  if (!(m < INFINITY)) s.S = NAN;  // +inf: the row is NaN
 
 #pragma unroll 1
   for (int blk = blk0; blk < blk1; ++blk) {
@@ -574,34 +603,31 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
       cp_async_wait_group<1>();
       read(blk);
       const int seen = blk - blk0;
-      if (a.k > 0 && seen == seen_by_bound * (a.k <= kFew ? 4 : 2)) {
-        raise();
-        seen_by_bound = seen;
-      }
+      if (a.k > 0 && seen > 1 && (seen & (seen - 1)) == 0 && (a.k > kFew || (seen & 0x55555555))) raise();
       mx = fmaxf(mx, vm);
       if (vm > s.mu) {
         if (vm < INFINITY) s.move(vm);
-        else inf = true;
-        lo = floor_of(s.mu);
+        else s.S = NAN;
       }
     }
-    if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0) {
+    if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0 && !a.rank_all) {
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
-        const bool in = !(max_of<T, 1>({cur[i]}) < tau_f);
+        const uint32_t at = (uint32_t)((blk - blk0) * kBlock + i * kThreads + t);
+        const bool in = !(max_of<T, 1>({cur[i]}) < tau_f) && row.column(run0 + at) < (int64_t)row.N;
         const uint32_t who = __ballot_sync(0xffffffffu, in);
         if (n_noted + __popc(who) > kList) {
           keep = look<T>(keep_buf[w], keep, noted[w], n_noted, row, run0, nullptr, ~0u, a.k);
           tau_f = key_value(keep.tau);
           n_noted = 0;
         }
-        if (in)
-          noted[w][n_noted + __popc(who & ((1u << lane) - 1))] = (uint32_t)((blk - blk0) * kBlock + i * kThreads + t);
+        if (in) noted[w][n_noted + __popc(who & ((1u << lane) - 1))] = at;
         n_noted += __popc(who);
       }
     }
     if (fabsf(s.mu) < kFar) {
       const f2 L = pair(kLog2e, kLog2e), R = pair(-s.R, -s.R);
+      const float lo = floor_of(s.mu);
       f2 S2 = 0, Y2 = 0;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
@@ -630,9 +656,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
     request(blk + kRing);
   }
   cp_async_wait_all();
-  uint64_t* flat = reinterpret_cast<uint64_t*>(ring);  // [kThreads], once every thread is through its blocks
-  if (a.k > 0) {
-    if (a.k > kFew && blk1 - blk0 > seen_by_bound) raise();
+  uint64_t* flat = a.rank_all ? keep_buf[0] : reinterpret_cast<uint64_t*>(ring);  // once every thread is through its blocks
+  if (a.k > 0 && !a.rank_all) {
+    if (a.k > kFew && blk1 - blk0 > 1) raise();
     keep = look<T>(keep_buf[w], keep, noted[w], n_noted, row, run0, &ring[0][0][0],
                    (uint32_t)max(blk1 - blk0 - kRing, 0) * kBlock, a.k);
   }
@@ -641,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   float mu = s.mu;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
-  inf = __any_sync(0xffffffffu, inf);
   __syncthreads();
   if (lane == 0) {
     red[0][w] = mu;
@@ -661,13 +686,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
     s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
     s.Y += __shfl_xor_sync(0xffffffffu, s.Y, o);
   }
-  if (inf) s.S = NAN;
   if (lane == 0) {
     red[1][w] = s.S;
     red[2][w] = s.Y;
   }
-  if (c <= kThreads)
+  if (a.rank_all) {
+    c = (int)row.N;
+  } else if (c <= kThreads) {
     for (int i = lane; i < keep.n; i += 32) flat[at + i] = keep_buf[w][i];
+  }
   __syncthreads();
   s.S = s.Y = 0.f;
 #pragma unroll
@@ -703,7 +730,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
   } else {
     uint64_t key[kCap / 32];
 #pragma unroll
-    for (int i = 0; i < kCap / 32; ++i) key[i] = i * 32 + lane < keep.n ? keep_buf[w][i * 32 + lane] : 0;
+    for (int i = 0; i < kCap / 32; ++i)
+      key[i] = a.rank_all                  ? (i * kThreads + t < c ? flat[i * kThreads + t] : 0)
+               : i * 32 + lane < keep.n ? keep_buf[w][i * 32 + lane]
+                                        : 0;
     emit_best(key, a.k, hist, found, best, &n_best, emit);
   }
 }
@@ -958,10 +988,14 @@ inline int64_t forward_runs(int B, int64_t blocks) {
   if (blocks <= 4 || (B >= 64 && blocks <= 8) || (B >= 128 && blocks <= 16)) return 1;
   return runs(B, blocks, 888, 2);
 }
-inline int64_t grad_runs(int B, int64_t blocks) { return runs(B, blocks, 1776, 1); }
+// The gradient has nothing to join: short runs, of which many are in flight (256 x
+// 670,208 bf16: 109 us with 14 a row, 117 with 7, 133 with one block each).
+inline int64_t grad_runs(int B, int64_t blocks) { return runs(B, blocks, 3552, 1); }
 
 template <typename T>
-cudaError_t launch(int B, const Args& a, cudaStream_t st) {
+cudaError_t launch(int B, Args a, cudaStream_t st) {
+  a.thin = a.N / (16 / (int)sizeof(T)) < a.k * (a.k <= kFew ? 4 : 2);
+  a.rank_all = a.k > 0 && a.n_run == 1 && (a.N <= 128 || a.N / (16 / (int)sizeof(T)) < a.k);
   return launch_early(k_logprob<T>, (unsigned)(B * (int64_t)a.n_run), kThreads, 0, st, a);
 }
 template <typename T>
