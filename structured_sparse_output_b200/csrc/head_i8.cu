@@ -186,6 +186,11 @@ cudaError_t launch_quantize(int64_t rows, int n, const void* x, int8_t* q, float
 //              TMEM accumulators of BN columns
 //   warps 2-9  epilogue: warp (q, half) reads lane quarter q of its half of the
 //              columns, scales and stores
+// 512 x 131,072 x 1024 to bf16: 74 us, 1.86 Pop/s, against 41 us for its bytes at a
+// copy's rate.  The MMAs alone take 49 us (199 clocks for 128 x 256 x 32), the whole
+// without loads 65 and without the epilogue 58: staging 48 KB for 4 MMAs, the MMAs and
+// the epilogue's TMEM reads share an SM's ports.  Up to some hundred samples the
+// weights' bytes bound it: 32 x 131,072 x 1024 in 29 us, 4.9 TB/s.
 constexpr int kThreads = 320;
 constexpr int kML = 128;      // labels per tile
 constexpr int kKB = 128;      // K bytes per stage
