@@ -123,8 +123,8 @@ __device__ __forceinline__ void row_list(const int32_t* row_ptr, int64_t nnz, in
                                          int64_t& end) {
   begin = end = 0;
   if (!row_ptr) return;
-  begin = row_ptr[b];
-  end = row_ptr[b + 1];
+  begin = __ldcg(row_ptr + b);
+  end = __ldcg(row_ptr + b + 1);
   begin = begin < 0 ? 0 : begin > nnz ? nnz : begin;
   end = end < begin ? begin : end > nnz ? nnz : end;
 }
@@ -247,14 +247,15 @@ __device__ __forceinline__ RowStats row_stats(float m, float S) {
   return r;
 }
 // The given labels of a row: each thread's first one is loaded early, since its logit
-// is found through two loads before it.
+// is found through two loads before it.  (From L2: the join loads them before it waits
+// for the kernel before it.)
 template <typename T>
 struct Given {
   int64_t begin, end;
   float z;  // of entry begin + threadIdx.x; NaN for an id outside the row
   __device__ float logit(const Args& a, const T* row, int64_t p) const {
-    const int64_t id = a.ids[p];
-    return id >= 0 && id < a.N ? Elem<T>::to_f(row[id]) : NAN;
+    const int64_t id = __ldcg(a.ids + p);
+    return id >= 0 && id < a.N ? Elem<T>::to_f(__ldcg(row + id)) : NAN;
   }
   __device__ Given(const Args& a, int64_t b, const T* row) {
     row_list(a.row_ptr, a.nnz, b, begin, end);
@@ -277,8 +278,19 @@ struct Given {
 // can be beaten by the others.
 struct Keep {
   int n;
+  bool strict;  // k kept keys reach tau: a later equal logit, of a larger id, is beaten
   uint64_t tau;
+  // The value that a logit has to reach from here on.
+  __device__ float bar() const { return key_value(strict ? ((tau >> 32) + 1) << 32 : tau); }
+  __device__ void raise(uint64_t to) {
+    if (to > tau) {
+      tau = to;
+      strict = false;
+    }
+  }
 };
+// -inf and NaN compete only where a run has fewer than k other logits.
+constexpr uint64_t kFinite = (uint64_t)0x00800000u << 32;
 
 // Raise tau until at most kRoom of the warp's keys reach it, and still k do.
 __device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
@@ -306,22 +318,21 @@ __device__ __noinline__ Keep shrink(uint64_t* buf, Keep s, int k) {
     at += __popc(who);
   }
   __syncwarp();
-  return Keep{at, c > s.tau ? c : s.tau};
+  return Keep{at, c >= s.tau || s.strict, c > s.tau ? c : s.tau};
 }
 
-// Add the logits of one vector of every lane (of those with `live`) that reach tau; a
-// NaN counts as -inf.
+// Add the logits of one vector of every lane (of those with `live`) that reach tau.
 template <typename T>
 __device__ __noinline__ Keep take(uint64_t* buf, Keep s, uint4 raw, bool live, int64_t j, uint32_t N, int k) {
   constexpr int kE = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   uint32_t hit = 0;
   if (live) {
-    const float tau_f = key_value(s.tau);
+    const float bar = s.bar();
     float v[kE];
     unpack<T>(raw, v);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) hit |= (v[e] >= tau_f || tau_f == -INFINITY) ? 1u << e : 0u;
+    for (int e = 0; e < kE; ++e) hit |= v[e] >= bar ? 1u << e : 0u;
   }
   while (__any_sync(0xffffffffu, hit != 0)) {
     uint64_t key = 0;
@@ -512,7 +523,8 @@ __device__ __noinline__ Keep look(uint64_t* buf, Keep s, const uint32_t* list, i
 // first block and again after 4, 16 .. blocks (more than 16 alternatives: after 2, 4,
 // 8 .. and at the end; raising the bound costs two barriers, about 0.4 us, and leaves
 // fewer logits to rank).  A warp notes the vectors whose maximum reaches the bound of
-// the time, and looks into them at the end (or when its list is full).
+// the time, and looks into them at the end (or when its list is full).  -inf does not
+// compete: where a run has fewer than k other logits, its first -inf or NaN follow.
 // 256 x 670,208 bf16 logits: 58 us without alternatives (5.9 TB/s, 90% of a copy's
 // rate; issuing the sums' instructions takes 80% of the cycles), 70 us with 5 (the
 // starts and ends of the runs, of which 4 CTAs share an SM).  Rows read three times by
@@ -581,19 +593,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[0][w] = m;
-  Keep keep{0, 0};
+  Keep keep{0, false, kFinite};
   float tau_f = INFINITY;
   auto raise = [&] {
-    const uint64_t up = (uint64_t)(a.k <= kFew ? bound_of<64>(mx, a.k, group, &tau_s)
-                                               : bound_of<128>(mx, a.k, group, &tau_s)) << 32;
-    if (up > keep.tau) keep.tau = up;
-    tau_f = key_value(keep.tau);
+    keep.raise((uint64_t)(a.k <= kFew ? bound_of<64>(mx, a.k, group, &tau_s)
+                                      : bound_of<128>(mx, a.k, group, &tau_s)) << 32);
+    tau_f = keep.bar();
   };
   if (a.k == 0 || a.rank_all) {
     __syncthreads();
   } else if (a.thin) {
-    keep.tau = (uint64_t)bound_thin(mx, a.k, group, &tau_s) << 32;
-    tau_f = key_value(keep.tau);
+    keep.raise((uint64_t)bound_thin(mx, a.k, group, &tau_s) << 32);
+    tau_f = keep.bar();
   } else {
     raise();
   }
@@ -616,15 +627,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
         else s.S = NAN;
       }
     }
-    if (__any_sync(0xffffffffu, !(vm < tau_f)) && a.k > 0 && !a.rank_all) {
+    if (__any_sync(0xffffffffu, vm >= tau_f) && a.k > 0 && !a.rank_all) {
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         const uint32_t at = (uint32_t)((blk - blk0) * kBlock + i * kThreads + t);
-        const bool in = !(max_of<T, 1>({cur[i]}) < tau_f) && row.column(run0 + at) < (int64_t)row.N;
+        const bool in = max_of<T, 1>({cur[i]}) >= tau_f;
         const uint32_t who = __ballot_sync(0xffffffffu, in);
         if (n_noted + __popc(who) > kList) {
           keep = look<T>(keep_buf[w], keep, noted[w], n_noted, row, run0, nullptr, ~0u, a.k);
-          tau_f = key_value(keep.tau);
+          tau_f = keep.bar();
           n_noted = 0;
         }
         if (in) noted[w][n_noted + __popc(who & ((1u << lane) - 1))] = at;
@@ -731,8 +742,21 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob(Args a) {
       for (int j = 0; j < c; ++j) rank += flat[j] > key;
       if (rank < a.k) emit(rank, key);
     }
-    if (a.n_run > 1)  // a short last run
-      for (int r = c + t; r < a.k; r += kThreads) keys[r] = 0;
+    if (c < a.k && w == 0) {
+      // fewer than k logits above -inf: the first of the others, -inf or NaN, follow
+      const int64_t j0 = max(row.column(run0), (int64_t)0);
+      const int64_t j1 = min(row.column((uint32_t)blk1 * kBlock), a.N);
+      int r = c;
+      for (int64_t j = j0 + lane; r < a.k && j - lane < j1; j += 32) {
+        const bool other = j < j1 && !(Elem<T>::to_f(row.z[j]) > -INFINITY);
+        const uint32_t who = __ballot_sync(0xffffffffu, other);
+        const int at = r + __popc(who & ((1u << lane) - 1));
+        if (other && at < a.k) emit(at, rank_key(-INFINITY, (uint32_t)j));
+        r += __popc(who);
+      }
+      if (a.n_run > 1)  // a short last run
+        for (r += lane; r < a.k; r += 32) keys[r] = 0;
+    }
   } else {
     uint64_t key[kCap / 32];
 #pragma unroll
