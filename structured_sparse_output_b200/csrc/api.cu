@@ -1128,6 +1128,18 @@ haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtyp
   DeviceInfo di;
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (head8::few(B, H, head8::pitch(d))) {  // quantised by the product's own CTAs
+    ProfScope ps("head_forward_i8", s);
+    cudaError_t e;
+    if (out_dt == HASTE_BF16)
+      e = dt == HASTE_BF16
+              ? head8::launch_few<__nv_bfloat16, __nv_bfloat16>(B, H, d, Xh, Wq, w_scale, logits, di.sms, s)
+              : head8::launch_few<__nv_bfloat16, float>(B, H, d, Xh, Wq, w_scale, logits, di.sms, s);
+    else
+      e = dt == HASTE_BF16 ? head8::launch_few<float, __nv_bfloat16>(B, H, d, Xh, Wq, w_scale, logits, di.sms, s)
+                           : head8::launch_few<float, float>(B, H, d, Xh, Wq, w_scale, logits, di.sms, s);
+    return e == cudaSuccess ? HASTE_OK : cuda_fail(e, "haste_head_forward_i8 launch");
+  }
   int8_t* qx = static_cast<int8_t*>(ws);
   float* sx = reinterpret_cast<float*>(qx + sc);
   cudaError_t e;

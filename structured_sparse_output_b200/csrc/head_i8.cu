@@ -459,6 +459,110 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------- the product of a few samples
+// Up to 4 samples: one launch without tensor cores, whose latencies (quantisation,
+// staging, MMA, TMEM) are most of a small call.  Every CTA quantises the samples into
+// shared memory, its first weights already on the way; a warp takes 4 labels at a
+// time, its lanes 16-byte pieces of their rows, and adds up 4-way byte products.
+// One sample, 4,096 labels x 768: 2.7 us (5.7 through the tiles); 131,072 x 1024:
+// 22.8 us, 5.9 TB/s (28.1).  Each sample adds its own shared-memory reads and byte
+// products: 4 samples take 4.2 us (5.6) and 28.7 (28.2), 8 would take 5.9 and 44.
+constexpr int kFewThreads = 256, kFewLabels = 4, kFewBytes = 32768;
+
+struct FewArgs {
+  int B, H, d;
+  bool vec;  // rows of x start on 16 bytes and hold whole vectors of 8
+  const int8_t* w;
+  const float* sw;
+  void* out;
+};
+
+template <typename O, typename T, int BT>
+__global__ void __launch_bounds__(kFewThreads, 2) k_head_i8_few(FewArgs a, const T* __restrict__ x) {
+  extern __shared__ __align__(16) uint8_t few_smem[];  // [BT][ld]
+  __shared__ uint32_t row_max_bits[BT];
+  __shared__ float sxs[BT];
+  constexpr int kRounds = 2;  // 512-byte runs of 4 labels' rows in registers
+  const int t = threadIdx.x, lane = t & 31, ld = pitch(a.d), n16 = ld / 16;
+  const int n_warps = gridDim.x * (kFewThreads / 32), first = blockIdx.x * (kFewThreads / 32) + (t >> 5);
+  const int groups = (a.H + kFewLabels - 1) / kFewLabels;
+  wait_for_stream();
+  let_next_start();
+  uint4 wv[kFewLabels][kRounds];
+  auto fetch = [&](int g, int c) {  // 16-byte pieces c + lane, c + 32 + lane of group g's rows
+#pragma unroll
+    for (int l = 0; l < kFewLabels; ++l) {
+      const int h = min(g * kFewLabels + l, a.H - 1);
+      const uint4* row = reinterpret_cast<const uint4*>(a.w + (int64_t)h * ld);
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int p = c + r * 32 + lane;
+        wv[l][r] = p < n16 ? row[p] : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  if (first < groups) fetch(first, 0);
+
+  // the samples, 8 elements at a time; past the last one zeros
+  if (t < BT) row_max_bits[t] = 0;
+  __syncthreads();
+  const int runs = ld / 8;
+  for (int i = t; i < a.B * runs; i += kFewThreads) {
+    float v[8];
+    load8(x + (int64_t)(i / runs) * a.d, i % runs * 8, a.d, a.vec, v);
+    atomicMax(&row_max_bits[i / runs], __float_as_uint(row_max(0.f, v)));
+  }
+  __syncthreads();
+  for (int i = t; i < BT * runs; i += kFewThreads) {
+    const int b = i / runs;
+    uint2 q = make_uint2(0, 0);
+    if (b < a.B) {
+      const RowScale s(__uint_as_float(row_max_bits[b]));
+      float v[8];
+      load8(x + (int64_t)b * a.d, i % runs * 8, a.d, a.vec, v);
+      q = s.quantised(v);
+      if (i % runs == 0) sxs[b] = s.s;
+    }
+    *reinterpret_cast<uint2*>(few_smem + b * ld + i % runs * 8) = q;
+  }
+  __syncthreads();
+
+  O* out = static_cast<O*>(a.out);
+  for (int g = first; g < groups; g += n_warps) {
+    int acc[kFewLabels][BT] = {};
+    for (int c = 0; c < n16; c += 32 * kRounds) {
+      if (c > 0) fetch(g, c);
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int p = c + r * 32 + lane;
+        if (c + r * 32 >= n16) break;
+#pragma unroll
+        for (int b = 0; b < BT; ++b) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(few_smem + b * ld + (p < n16 ? p : 0) * 16);
+#pragma unroll
+          for (int l = 0; l < kFewLabels; ++l) {
+            acc[l][b] = __dp4a((int)wv[l][r].x, (int)xv.x, acc[l][b]);
+            acc[l][b] = __dp4a((int)wv[l][r].y, (int)xv.y, acc[l][b]);
+            acc[l][b] = __dp4a((int)wv[l][r].z, (int)xv.z, acc[l][b]);
+            acc[l][b] = __dp4a((int)wv[l][r].w, (int)xv.w, acc[l][b]);
+          }
+        }
+      }
+    }
+    if (g + n_warps < groups) fetch(g + n_warps, 0);
+    int mine = 0;  // of label lane % 4 and sample lane / 4
+#pragma unroll
+    for (int l = 0; l < kFewLabels; ++l)
+#pragma unroll
+      for (int b = 0; b < BT; ++b) {
+        const int s = __reduce_add_sync(0xffffffffu, acc[l][b]);
+        if (lane == b * kFewLabels + l) mine = s;
+      }
+    const int h = g * kFewLabels + lane % kFewLabels, b = lane / kFewLabels;
+    if (b < a.B && b < BT && h < a.H) out[(int64_t)b * a.H + h] = Elem<O>::from_f((float)mine * (sxs[b] * a.sw[h]));
+  }
+}
+
 // 2D map of rows of ld bytes in boxes of 128 bytes x box_rows (128B swizzle), zeros
 // past the edges.
 inline cudaError_t tmap_i8(CUtensorMap* tm, const void* base, uint64_t ld, uint64_t rows, uint32_t box_rows) {
@@ -485,6 +589,34 @@ cudaError_t launch_product_t(Args a, int ld, const int8_t* qx, const int8_t* qw,
     e = set_once(done, reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<BN>());
   if (e != cudaSuccess) return e;
   return launch_early(kern, (unsigned)(a.n_tiles < sms ? a.n_tiles : sms), kThreads, smem_bytes<BN>(), st, a, tm_w, tm_x);
+}
+
+// Where the tiles are slower: up to 16,384 labels (two launches against one), and one
+// or two samples of rows long enough to occupy a warp's lanes (1 x 131,072 x 1024 22.8
+// and 28.1 us, but x 256 13.6 and 10.4 us).  Three and four samples of more than 1,024
+// features take as long as the tiles, or longer (4 x 16,384 x 4096: 24 and 18 us).
+inline int few_samples(int B) { return B <= 2 ? B : 4; }
+inline bool few(int B, int H, int ld) {
+  if (B > 4 || few_samples(B) * ld > kFewBytes) return false;
+  return B <= 2 ? H <= 16384 || ld >= 768 : H <= 16384 && ld <= 1024;
+}
+
+template <typename O, typename T, int BT>
+cudaError_t launch_few_t(const FewArgs& a, const T* x, int sms, cudaStream_t st) {
+  const int per_cta = kFewLabels * kFewThreads / 32, want = (a.H + per_cta - 1) / per_cta;
+  return launch_early(k_head_i8_few<O, T, BT>, (unsigned)(want < 2 * sms ? want : 2 * sms), kFewThreads,
+                      (size_t)BT * pitch(a.d), st, a, x);
+}
+template <typename O, typename T>
+cudaError_t launch_few(int B, int H, int d, const void* x, const int8_t* qw, const float* sw, void* out, int sms,
+                       cudaStream_t st) {
+  const FewArgs a{B, H, d, reinterpret_cast<uintptr_t>(x) % 16 == 0 && d % 8 == 0, qw, sw, out};
+  const T* xp = static_cast<const T*>(x);
+  switch (few_samples(B)) {
+    case 1: return launch_few_t<O, T, 1>(a, xp, sms, st);
+    case 2: return launch_few_t<O, T, 2>(a, xp, sms, st);
+    default: return launch_few_t<O, T, 4>(a, xp, sms, st);
+  }
 }
 
 // Samples per tile: the width (not above the batch's, rounded up) whose rounds of tiles

@@ -111,7 +111,10 @@ def _check(out, x64, q, s, out_dt):
 HEADS = [(1, 1, 1), (1, 4096, 768), (2, 100, 17), (3, 129, 128), (16, 128, 16), (17, 300, 130), (37, 10_007, 1000),
          (64, 1024, 256), (65, 257, 4096), (100, 500, 200), (128, 4096, 768), (129, 640, 384), (200, 333, 777),
          (256, 1000, 768), (257, 1000, 1024), (300, 77, 31), (512, 2049, 1024), (700, 260, 100), (1000, 40, 64),
-         # many samples and labels: tiles shared by CTA pairs, one and several a pair, ragged in each direction
+         # few samples, one launch: each width, rows of one and several rounds, more labels than warps
+         (1, 3, 4096), (2, 5000, 1040), (4, 30_001, 96), (5, 513, 2000), (7, 64, 4096), (8, 4099, 1500), (8, 70, 4097),
+         (1, 50, 32_768), (1, 77, 32_769), (3, 40_007, 33), (3, 5001, 1000), (4, 16_384, 20), (2, 70_001, 800),
+         # many samples and labels, one and several tiles a CTA, ragged in each direction
          (129, 8192, 16), (256, 8200, 768), (200, 16_513, 130), (384, 9001, 777), (512, 40_000, 256), (1025, 8321, 300)]
 
 

@@ -144,6 +144,41 @@ def test_logprob_patterns_ties_and_masks(N, dt):
         _check(_run(zt, rp, ids, k), z, rp, ids, k)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_logprob_short_rows(dt):
+    """Row lengths and numbers of alternatives around the changes of method: every logit
+    ranked, groups of one thread, of several; random, tied, ascending and masked rows."""
+    for N in (2, 7, 8, 9, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 300, 511, 512, 513, 700, 1024, 1025, 2047, 2049):
+        rng = np.random.default_rng(N)
+        r = rng.standard_normal((6, N)) * 2
+        r[1] = np.round(r[1])
+        r[2] = np.sort(r[2])
+        r[3, rng.random(N) < 0.9] = -np.inf
+        r[4] = 0.5
+        r[5, N // 2:] = np.nan
+        zt, z = _logits(r, dt, offset=N % 5)
+        rp, ids = _lists([2] * 6, N, rng)
+        for k in sorted({min(k, N) for k in (1, 5, 16, 17, 40, 64)}):
+            _check(_run(zt, rp, ids, k), z, rp, ids, k)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_logprob_runs_with_few_or_no_finite_logits(dt):
+    """Rows split into runs of which most are masked: the alternatives come from one run,
+    from several, or are masked labels in the order of their ids."""
+    N, k = 400_003, 64
+    r = np.full((5, N), -np.inf)
+    r[0, 399_000:399_100] = np.linspace(0, 1, 100)
+    r[1, ::20_001] = np.arange(len(range(0, N, 20_001)))
+    r[2, N - 1] = 3.0
+    r[3, 200_000:200_040] = 1.0
+    r[4, :30] = np.nan
+    zt, z = _logits(r, dt, offset=3)
+    rp, ids = _lists([2] * 5, N, np.random.default_rng(0))
+    for kk in (1, 7, k):
+        _check(_run(zt, rp, ids, kk), z, rp, ids, kk)
+
+
 def test_logprob_lists_out_of_range_ids_and_odd_row_ptr():
     rng = np.random.default_rng(3)
     zt, z = _logits(rng.standard_normal((4, 50)), "f32")
