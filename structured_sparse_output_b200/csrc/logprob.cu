@@ -919,16 +919,28 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   const float gH = a.d_entropy ? a.d_entropy[b] : 0.f, H = a.d_entropy ? a.entropy[b] : 0.f;
   int64_t p0, p1;
   row_list(a.row_ptr, a.nnz, b, p0, p1);
-  float G = 0.f;  // every warp sums the list in the same order
+  // every warp sums the list, in the same order; long ones are split over the warps
+  // (64 x 32,768, 4,096 labels a row: 12.0 us against 21.0)
+  __shared__ float g_warp[kWarps];
+  const bool split = p1 - p0 > 4 * 32;
+  float G = 0.f;
   bool ascending = true;
-  for (int64_t p = p0 + (t & 31); p < p1; p += 32) {
+  for (int64_t p = p0 + (split ? t : t & 31), step = split ? kThreads : 32; p < p1; p += step) {
     const int64_t id = a.ids[p];
     if (id >= 0 && id < a.N) G += a.d_logp[p];
     ascending &= p + 1 == p1 || id < a.ids[p + 1];
   }
-  ascending = __all_sync(0xffffffffu, ascending);  // then no label is given twice
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
+  if (split) {
+    if ((t & 31) == 0) g_warp[t >> 5] = G;
+    ascending = __syncthreads_and(ascending);
+    G = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) G += g_warp[i];
+  } else {
+    ascending = __all_sync(0xffffffffu, ascending);  // then no label is given twice
+  }
   // the definition, for single labels and where R would lose too much
   auto dense = [&](float v) {
     const float lp = v - lse, p = ex2(lp * kLog2e);
@@ -981,19 +993,68 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
     }
   }
   if (p0 == p1 || none) return;
+  __syncthreads();  // the dense term is written
+  const int64_t c0 = max(row.column((uint32_t)blk0 * kBlock), (int64_t)0);
+  const int64_t c1 = min(row.column((uint32_t)blk1 * kBlock), a.N);
+  auto put = [&](int64_t id, float g) { dz[id] = Elem<T>::from_f(g + dense(Elem<T>::to_f(row.z[id]))); };
+  if (ascending) {
+    for (int64_t p = p0 + t; p < p1; p += kThreads) {
+      const int64_t id = a.ids[p];
+      if (id >= c0 && id < c1) put(id, a.d_logp[p]);
+    }
+    return;
+  }
+  // Any other list: a label that may be given again (it shares its bit of `again` with a
+  // second entry) is looked for in the whole list by its warp, and its first entry takes
+  // the sum.  (Every label looked for by its thread: 256 x 8,192, 1,024 shuffled labels
+  // a row, 154 us against 8.7; in ascending order 6.4.)
+  constexpr uint32_t kBits = 32768;
+  __shared__ uint32_t once[kBits / 32], again[kBits / 32];
+  for (int i = t; i < (int)(kBits / 32); i += kThreads) once[i] = again[i] = 0;
   __syncthreads();
-  const int64_t c0 = row.column((uint32_t)blk0 * kBlock), c1 = row.column((uint32_t)blk1 * kBlock);
   for (int64_t p = p0 + t; p < p1; p += kThreads) {
     const int64_t id = a.ids[p];
-    if (id < 0 || id >= a.N || id < c0 || id >= c1) continue;
-    float g = ascending ? a.d_logp[p] : 0.f;
-    bool first = true;
-    for (int64_t q = p0; q < p1 && !ascending; ++q)
-      if (a.ids[q] == id) {
-        if (q < p) first = false;
-        g += a.d_logp[q];
+    if (id < c0 || id >= c1) continue;
+    const uint32_t at = (uint32_t)id % kBits, bit = 1u << at % 32;
+    if (atomicOr(&once[at / 32], bit) & bit) atomicOr(&again[at / 32], bit);
+  }
+  __syncthreads();
+  for (int64_t q0 = p0 + (t & ~31); q0 < p1; q0 += kThreads) {
+    const int64_t p = q0 + (t & 31), id = p < p1 ? a.ids[p] : -1;
+    const uint32_t at = (uint32_t)id % kBits;
+    const bool here = id >= c0 && id < c1, look_for = here && (again[at / 32] >> at % 32 & 1);
+    if (here && !look_for) put(id, a.d_logp[p]);
+    for (uint32_t todo = __ballot_sync(0xffffffffu, look_for); todo; todo &= todo - 1) {
+      const int l = __ffs(todo) - 1;
+      const int label = __shfl_sync(0xffffffffu, (int)id, l);
+      bool first = true;
+      float g = 0.f;
+      for (int64_t q = p0; q < p1; q += 4 * 32) {
+        bool hit[4];
+        uint32_t who[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t r = q + i * 32 + (t & 31);
+          hit[i] = r < p1 && a.ids[r] == label;
+        }
+        if (!__any_sync(0xffffffffu, hit[0] || hit[1] || hit[2] || hit[3])) continue;
+        int64_t at0 = q;  // the first entry among these that gives the label
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          who[i] = __ballot_sync(0xffffffffu, hit[i]);
+          if (who[i]) at0 = q + i * 32 + __ffs(who[i]) - 1;
+        }
+        first = at0 >= q0 + l;
+        if (!first) break;
+        float add[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add[i] = hit[i] ? a.d_logp[q + i * 32 + (t & 31)] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          for (; who[i]; who[i] &= who[i] - 1) g += __shfl_sync(0xffffffffu, add[i], __ffs(who[i]) - 1);
       }
-    if (first) dz[id] = Elem<T>::from_f(g + dense(Elem<T>::to_f(row.z[id])));
+      if (first && (t & 31) == l) put(label, g);
+    }
   }
 }
 

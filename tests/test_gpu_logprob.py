@@ -299,6 +299,34 @@ def test_gradient_long_list_and_no_terms():
     assert not dz.any()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [60, 33_000, 140_003])
+def test_gradient_lists_in_any_order(N, dt):
+    """Long and short lists that do not ascend: shuffled without a repeat, labels 32,768
+    apart, one label throughout, two in turn, a repeat at both ends, ids outside the row."""
+    rng = np.random.default_rng(N + 1)
+    apart = np.arange(N % 32_768 % 50, N, 32_768)
+    lists = [rng.permutation(N)[:n] for n in (31, 32, 33, 60, 127, 128, 129, 300, 2_000)]
+    lists += [rng.permutation(np.concatenate([apart, apart, rng.integers(0, N, 200)])), np.full(700, N - 1),
+              np.tile([N - 1, 0], 130), rng.integers(0, N, 515), np.array([3, 2]), np.array([2, 2]), np.arange(50)[::-1],
+              np.arange(0), rng.integers(-N, 2 * N, 400)]
+    end = rng.permutation(N)[:257]
+    end[-1] = end[0]
+    lists.append(end)
+    rp = np.concatenate([[0], np.cumsum([len(x) for x in lists])]).astype(np.int32)
+    ids = np.concatenate(lists).astype(np.int32)
+    zt, z = _logits(rng.standard_normal((len(lists), N)) * 2, dt, offset=3)
+    g, gh = rng.standard_normal(len(ids)).astype(np.float32), rng.standard_normal(len(z)).astype(np.float32)
+    _, lse, ent, _, _ = _run(zt, rp, np.clip(ids, 0, N - 1), 0)
+    outs = []
+    for _ in range(2):
+        dz = torch.full_like(zt, 9.0)
+        H.haste_logprob_backward(zt, lse, ent, _dev(rp), _dev(ids), _dev(g), _dev(gh), dz)
+        outs.append(dz)
+    assert torch.equal(*outs)
+    _check_grad(to_np64(outs[0]), z, rp, ids, g, gh, dt)
+
+
 def test_gradient_against_differences():
     """Central differences of the GPU's own forward values on fp32 logits."""
     rng = np.random.default_rng(9)
