@@ -162,6 +162,35 @@ def test_logprob_short_rows(dt):
             _check(_run(zt, rp, ids, k), z, rp, ids, k)
 
 
+def _many_short_rows(B, N, rng):
+    """Random, rounded, ascending, mostly masked, constant, NaN, fully masked, lowest-value
+    and far rows in turn."""
+    r = rng.standard_normal((B, N)) * 2
+    r[1::9] = np.round(r[1::9])
+    r[2::9] = np.sort(r[2::9])
+    r[3::9][rng.random(r[3::9].shape) < 0.95] = -np.inf
+    r[4::9] = 0.5
+    r[5::9, N // 2:] = np.nan
+    r[6::9] = -np.inf
+    r[7::9][rng.random(r[7::9].shape) < 0.5] = -3.3895313892515355e38      # the lowest value of both types
+    r[8::9] += 70_000
+    return r
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [33, 128, 129, 500, 1000, 1024, 1025, 2040, 2048, 2049, 4000, 4089, 4096, 4097])
+def test_logprob_many_short_rows(n, dt):
+    """Batches of rows of up to 8 KB, one after another and on and off the 16-byte boundary."""
+    N = n if dt == "bf16" or n < 130 else n // 2
+    B = 1030 if n < 2049 else 1027
+    rng = np.random.default_rng(n)
+    zt, z = _logits(_many_short_rows(B, N, rng), dt, offset=n % 2 * 3)
+    rp, ids = _lists(rng.integers(0, 5, B), N, rng, messy=True)
+    for k in (0, 1, 9, 32, 64):
+        if k <= N:
+            _check(_run(zt, rp, ids, k), z, rp, ids, k)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_logprob_runs_with_few_or_no_finite_logits(dt):
     """Rows split into runs of which most are masked: the alternatives come from one run,
@@ -244,6 +273,9 @@ def _check_grad(got, z, rp, ids, g, gh, dt):
     m = 8 + int(np.diff(rp).max(initial=0))                       # terms of the sums over a row's list
     tol = (torch.finfo(DT[dt]).eps / 2 * np.where(np.isfinite(ref), np.abs(ref), 0) + U * m * Ga
            + U * (m + 8 + 2 * zf + 4 * np.abs(fin)) * 2 * p * c + 1e-37)
+    # c can be 0 (one label left: log p = H = 0) while log p is rounded: lse = m + log S
+    # twice, 2 u |lse|, and z - lse once, u (|z| + |lse|); its part of c is gH times that.
+    tol = tol + p * gha[:, None] * U * (zf + 3 * np.abs(fin))
     _near(got, ref, tol, "d_logits")
 
 
@@ -297,6 +329,31 @@ def test_gradient_long_list_and_no_terms():
     _check_grad(to_np64(dz), z, rp, ids, g, None, "f32")
     H.haste_logprob_backward(zt, lse, None, None, None, None, None, dz)
     assert not dz.any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 33, 1000, 1025, 2048, 4089, 4096])
+def test_gradient_many_short_rows(n, dt):
+    N = n if dt == "bf16" or n < 130 else n // 2
+    B = 1030
+    rng = np.random.default_rng(n + 5)
+    r = _many_short_rows(B, N, rng)
+    zt, z = _logits(r, dt, offset=n % 2 * 3)
+    counts = rng.integers(0, 5, B)
+    counts[::50] = rng.integers(30, 600, len(counts[::50]))                # with repeats, in any order
+    rp, ids = _lists(counts, N, rng, messy=True)
+    for b in range(0, B, 3):
+        ids[rp[b]:rp[b + 1]] = np.sort(ids[rp[b]:rp[b + 1]])
+    ids[rng.random(len(ids)) < 0.02] = N + 7
+    g, gh = rng.standard_normal(len(ids)).astype(np.float32), rng.standard_normal(B).astype(np.float32)
+    _, lse, ent, _, _ = _run(zt, rp, np.minimum(ids, N - 1), 0)
+    buf = torch.full((B * N + 32,), 55.0, dtype=DT[dt], device="cuda")
+    for off in (0, n % 2 * 3):
+        dz = buf[off:off + B * N].view(B, N)
+        H.haste_logprob_backward(zt, lse, ent, _dev(rp), _dev(ids), _dev(g), _dev(gh), dz)
+        _check_grad(to_np64(dz), z, rp, ids, g, gh, dt)
+        assert (buf[off + B * N:] == 55).all()
+        buf.fill_(55.0)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
