@@ -192,6 +192,35 @@ def test_logprob_many_short_rows(n, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [70, 700, 1400, 2000])
+def test_logprob_and_gradient_of_short_rows_with_infinities(N, dt):
+    """+inf, NaN and one or two finite logits in the first, a middle and the last column."""
+    rng = np.random.default_rng(N)
+    B = 1200
+    r = rng.standard_normal((B, N))
+    col = np.array([0, N // 2, N - 1])[np.arange(B) % 3]
+    one = np.arange(B)
+    r[one[0::4], col[0::4]] = np.inf
+    r[one[1::4], col[1::4]] = np.nan
+    keep = r[one[2::4], col[2::4]]
+    r[2::4] = -np.inf
+    r[one[2::4], col[2::4]] = keep
+    zt, z = _logits(r, dt, offset=N % 3)
+    rp, ids = _lists([2] * B, N, rng)
+    for k in (1, 6, 33):
+        _check(_run(zt, rp, ids, k), z, rp, ids, k)
+    _, lse, ent, _, _ = _run(zt, rp, ids, 0)
+    g, gh = rng.standard_normal(len(ids)).astype(np.float32), rng.standard_normal(B).astype(np.float32)
+    dz = torch.empty_like(zt)
+    H.haste_logprob_backward(zt, lse, ent, _dev(rp), _dev(ids), _dev(g), _dev(gh), dz)
+    got, ref = to_np64(dz), O.logprob_backward(z, rp, ids, g, gh)
+    bad = np.isnan(ref).any(1)
+    assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
+    _check_grad(got[~bad], z[~bad], np.arange(0, 2 * (~bad).sum() + 1, 2), ids.reshape(B, 2)[~bad].reshape(-1),
+                g.reshape(B, 2)[~bad].reshape(-1), gh[~bad], dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_logprob_runs_with_few_or_no_finite_logits(dt):
     """Rows split into runs of which most are masked: the alternatives come from one run,
     from several, or are masked labels in the order of their ids."""
