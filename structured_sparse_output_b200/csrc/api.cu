@@ -1175,7 +1175,7 @@ static haste_status_t check_logprob(int B, int64_t N, haste_dtype_t dt, const ha
 // Workspace of haste_logprob: the sums and the rank keys of each run of rows that
 // are split.
 static size_t logprob_ws(int B, int64_t N, haste_dtype_t dt, int k, size_t* keys) {
-  const int64_t n = logprob::forward_runs(B, logprob_blocks(nullptr, N, dt));
+  const int64_t n = logprob::forward_runs(B, logprob_blocks(nullptr, N, dt), N * elem_bytes(dt));
   *keys = n > 1 ? align256((size_t)B * n * 16) : 0;
   return n > 1 ? *keys + align256((size_t)B * n * k * 8) : 0;
 }
@@ -1195,7 +1195,7 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void*
   if (!logits || (nnz > 0 && !logp) || (k > 0 && (!top_logp || !top_id)))
     return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
   if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
-  const int n_run = (int)logprob::forward_runs(B, logprob_blocks(logits, N, dt));
+  const int n_run = (int)logprob::forward_runs(B, logprob_blocks(logits, N, dt), N * elem_bytes(dt));
   size_t keys;
   if ((st = check_ws(ws, ws_bytes, logprob_ws(B, N, dt, k, &keys))) != HASTE_OK) return st;
   if (n_run > 1 && (st = check_aligned(ws, 16, "the workspace")) != HASTE_OK) return st;

@@ -1306,8 +1306,14 @@ inline int64_t runs(int B, int64_t blocks, int64_t ctas, int64_t least) {
 // against split: 256 x 65,536 bf16 13.1 and 20.4 us, 256 x 131,072 20.1 and 25.2 us,
 // 64 x 32,003 8.7 and 9.4 us; but 1 x 65,536 9.6 and 6.9 us, 256 x 670,208 (4 runs)
 // 87 and 73 us.
-inline int64_t forward_runs(int B, int64_t blocks) {
+// One block a run (the last half a block to one and a half, so that none is empty
+// wherever the rows start) where that leaves no more CTAs than SMs: 8 x 65,536 bf16 7.2 us with 5 alternatives, 10.0 with 64, against 8.5 and 11.4 in
+// runs of two.
+constexpr int64_t kSpread = 148;
+inline int64_t forward_runs(int B, int64_t blocks, int64_t row_bytes) {
   if (blocks <= 4 || (B >= 64 && blocks <= 8) || (B >= 128 && blocks <= 16)) return 1;
+  const int64_t single = (row_bytes + 8 * kBlock) / (16 * kBlock);
+  if (single <= kSpread / B) return single;
   return runs(B, blocks, 888, 2);
 }
 // The gradient has nothing to join: short runs, of which many are in flight (256 x

@@ -221,6 +221,25 @@ def test_logprob_and_gradient_of_short_rows_with_infinities(N, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("blocks", [5, 9, 37])
+def test_logprob_few_long_rows_around_whole_blocks(blocks, dt):
+    """Rows in runs of one 16 KB block, whose last one is short, whole or longer; rows that
+    start anywhere; more alternatives than runs and fewer."""
+    per = 8192 if dt == "bf16" else 4096
+    rng = np.random.default_rng(blocks)
+    for more in (0, 1, per // 2 - 1, per // 2, per // 2 + 1, per - 1):
+        N, B = blocks * per + more, 3 if blocks < 30 else 2
+        r = rng.standard_normal((B, N)) * 2
+        r[0] = np.round(r[0])
+        r[1, : N - 30] = -np.inf
+        for off in (0, more % 7 + 1):
+            zt, z = _logits(r, dt, offset=off)
+            rp, ids = _lists([3] * B, N, rng)
+            for k in (0, 1, 20, 64):
+                _check(_run(zt, rp, ids, k), z, rp, ids, k)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_logprob_runs_with_few_or_no_finite_logits(dt):
     """Rows split into runs of which most are masked: the alternatives come from one run,
     from several, or are masked labels in the order of their ids."""
