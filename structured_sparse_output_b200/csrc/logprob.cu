@@ -429,18 +429,23 @@ constexpr float kFar = 65536.f;
 // lost in rounding is put back once, by settle().
 struct Sums {
   float mu, R, S, Y;
-  __device__ explicit Sums(float m) : mu(m), R(m * kLog2e), S(0.f), Y(0.f) {}
+  // R is rounded by itself: fused into a later subtraction, it would not be the R of y
+  __device__ explicit Sums(float m) : mu(m), S(0.f), Y(0.f) { R = __fmul_rn(m, kLog2e); }
+  // What R lost: y is (z - mu) log2(e) + lost().  Nothing beyond kFar, where y has no R.
+  __device__ float lost() const { return fabsf(mu) < kFar ? fmaf(mu, kLog2e, -R) : 0.f; }
   __device__ void move(float to) {  // to >= mu
-    const float r = to * kLog2e;
-    const float d = fmaxf(fabsf(mu) < kFar && fabsf(to) < kFar ? R - r : (mu - to) * kLog2e, -300.f), w = ex2(d);
+    const Sums next(to);
+    // where one of the two lies beyond kFar, the sums take on what its y has and theirs not
+    const float far = (mu - to) * kLog2e + (next.lost() - lost());
+    const float d = fmaxf(fabsf(mu) < kFar && fabsf(to) < kFar ? R - next.R : far, -300.f), w = ex2(d);
     Y = w * fmaf(S, d, Y);
     S *= w;
     mu = to;
-    R = r;
+    R = next.R;
   }
   // S = sum e^(z - mu) and T = sum e^(z - mu) (mu - z)
   __device__ float settle() {
-    const float d = fabsf(mu) < kFar ? fmaf(mu, kLog2e, -R) : 0.f, w = ex2(-d);
+    const float d = lost(), w = ex2(-d);
     S *= w;
     return -kLn2 * fmaf(-d, S, w * Y);
   }
