@@ -324,9 +324,9 @@ def logprob(logits, row_ptr, ids, k: int):
             lse[b], entropy[b] = -np.inf, 0.0
             logp = np.full(N, -np.inf)
         else:
-            e = np.exp(r - m)
-            lse[b] = m + np.log(e.sum())
-            logp = r - lse[b]
+            log_s = np.log(np.exp(r - m).sum())
+            lse[b] = m + log_s
+            logp = (r - m) - log_s  # not r - lse, which loses log S far from zero
             p = np.exp(logp)
             entropy[b] = -np.sum(p * np.where(p > 0, logp, 0.0))
         rank = np.argsort(-np.where(np.isnan(r), -np.inf, r), kind="stable")[:k]
@@ -347,7 +347,9 @@ def logprob_backward(logits, row_ptr, ids, d_logp, d_entropy=None) -> np.ndarray
     for b in range(B):
         if lse[b] == -np.inf:
             continue
-        logp = z[b] - lse[b]
+        m = np.max(z[b])
+        with np.errstate(invalid="ignore"):  # +inf in a row: NaN
+            logp = (z[b] - m) - np.log(np.exp(z[b] - m).sum())
         p = np.exp(logp)
         mine = [i for i in range(row_ptr[b], row_ptr[b + 1]) if 0 <= ids[i] < N]
         c = float(sum(float(d_logp[i]) for i in mine))

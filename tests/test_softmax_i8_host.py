@@ -199,3 +199,16 @@ def test_valid_calls_need_a_device():
         pytest.skip("a GPU is present")
     for call in (_quantize, _head, _logprob, _grad):
         assert call() == H.HASTE_ERR_CUDA
+
+
+def test_oracle_softmax_does_not_depend_on_where_the_logits_lie():
+    """Rows of the types' lowest value and rows around 1e30, where a log sum of 8 is lost in
+    fp64: log p, the entropy and the gradient are those of the same row around 0."""
+    low = -3.3895313892515355e38
+    for z in (np.full((1, 8), low), np.full((1, 8), 1e30), np.full((1, 8), float(np.finfo(np.float32).max))):
+        lp, _, h, tl, _ = O.logprob(z, [0, 1], [3], 2)
+        assert np.allclose(lp, -np.log(8)) and np.allclose(tl, -np.log(8)) and np.isclose(h[0], np.log(8))
+        dz = O.logprob_backward(z, [0, 1], [3], [1.0], [2.0])
+        assert np.allclose(dz, np.eye(8)[3] - 1 / 8)
+    z = np.where(np.arange(8) % 2, low, -np.inf)[None]
+    assert np.allclose(O.logprob_backward(z, [0, 1], [3], [1.0]), np.eye(8)[3] - (np.arange(8) % 2) / 4)
