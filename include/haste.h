@@ -376,7 +376,10 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dtype, const vo
  *                    - p[b, j] * (G[b] + d_entropy[b] * (log p[b, j] + entropy[b])),
  *   G[b] = sum of row b's d_logp,
  * in the logits' dtype, ready for haste_head_backward, haste_backward_dw and
- * haste_backward_dx.  lse and entropy are haste_logprob's.  Masked labels get 0
+ * haste_backward_dx.  lse and entropy are haste_logprob's; p = e^(z - lse) is off by
+ * 2^-24 |lse| of itself, since lse is one fp32 number, and where |lse| >= 65536 the
+ * row's sum is taken again (rows of nothing but the type's lowest value have p =
+ * 1 / N).  Masked labels get 0
  * (and their own d_logp where they are given); rows of nothing but -inf get 0;
  * ids outside [0, N) count for nothing.  The choice of alternatives (top_*) has no
  * gradient.  The sums run in the order of the lists: repeats give the same bits.

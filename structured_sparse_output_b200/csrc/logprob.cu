@@ -1036,17 +1036,32 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_logprob_rows(Args a, int B) 
   if (keep.n < a.k) fill_others(row, 0, a.N, keep.n, a.k, emit);
 }
 
+// Beyond kFar an fp32 lse is too coarse to hold log S (of a row of the type's lowest value it
+// holds nothing of it).  What it lacks is the log of the row's sum of e^(z - lse), which
+// the threads of a row's warp or of each of its CTAs take again: this is their part of it.
+__device__ __forceinline__ bool lacks(float lse) { return fabsf(lse) >= kFar && fabsf(lse) < INFINITY; }
+template <typename T, int kStep>
+__device__ __noinline__ double far_sum(const Row<T> row, float lse) {
+  const uint32_t n_vec = (uint32_t)((row.N + (int64_t)row.head + Row<T>::kE - 1) / Row<T>::kE);
+  double S = 0.;
+  for (uint32_t v = threadIdx.x % kStep; v < n_vec; v += kStep) S += far_sums<T>(row.load(v), lse).x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+  return S;
+}
+__device__ __forceinline__ float lack_of(double S) { return S > 0. ? logf((float)S) : 0.f; }
+
 // The dense term of a row's gradient.  With y = z log2(e) - R, R = fl(lse log2(e)) and
 // e = lse log2(e) - R, which an fma gives exactly, p = 2^(y - e) and log p = ln2 (y - e):
 // the term is -2^y (A + C y) with A and C of the row.
 template <typename T>
 struct Dense {
   static constexpr int kE = 16 / sizeof(T), kP = kE / 2;
-  float lse, H, gH, G, lo;
+  float lse, lack, H, gH, G, lo;
   bool none, near;
   f2 R2, A2, C2;
-  __device__ Dense(float lse_, float H_, float gH_, float G_)
-      : lse(lse_), H(H_), gH(gH_), G(G_), lo(floor_of(lse_)), none(lse_ == -INFINITY),
+  __device__ Dense(float lse_, float lack_, float H_, float gH_, float G_)
+      : lse(lse_), lack(lack_), H(H_), gH(gH_), G(G_), lo(floor_of(lse_)), none(lse_ == -INFINITY),
         near(fabsf(lse_) < kFar || lse_ != lse_) {
     const float R = lse * kLog2e, e0 = fmaf(lse, kLog2e, -R), w = -ex2(-e0);
     const float A = w * fmaf(gH, fmaf(-kLn2, e0, H), G), C = w * gH * kLn2;
@@ -1056,7 +1071,7 @@ struct Dense {
   }
   // the definition, for single labels and where R would lose too much
   __device__ float at(float v) const {
-    const float lp = v - lse, p = ex2(lp * kLog2e);
+    const float lp = (v - lse) - lack, p = ex2(lp * kLog2e);
     return p == 0.f || none ? 0.f : -p * fmaf(gH, lp + H, G);
   }
   __device__ void of(const uint4& raw, float (&v)[kE]) const {
@@ -1219,7 +1234,17 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   } else {
     ascending = __all_sync(0xffffffffu, ascending);
   }
-  const Dense<T> dense(lse, H, gH, G);
+  float lack = 0.f;
+  if (lacks(lse)) {
+    __shared__ double far_warp[kWarps];
+    double S = far_sum<T, kThreads>(row, lse);
+    if ((t & 31) == 0) far_warp[t >> 5] = S;
+    __syncthreads();
+    S = 0.;
+    for (int i = 0; i < kWarps; ++i) S += far_warp[i];
+    lack = lack_of(S);
+  }
+  const Dense<T> dense(lse, lack, H, gH, G);
   // the output may sit on the 16-byte boundary differently from the input
   const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
   uint4* out_row = reinterpret_cast<uint4*>(dz - row.head) + t;
@@ -1273,7 +1298,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_logprob_grad_rows(GradArgs a
   bool ascending;
   const float G = list_sum(a, p0, p1, lane, 32, ascending);
   ascending = __all_sync(0xffffffffu, ascending);
-  const Dense<T> dense(lse, H, gH, G);
+  const Dense<T> dense(lse, lacks(lse) ? lack_of(far_sum<T, 32>(row, lse)) : 0.f, H, gH, G);
   const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
 #pragma unroll
   for (int i = 0; i < kN; ++i) {

@@ -33,10 +33,12 @@ def _need_gpu():
 def _check(out, z, rp, ids, k):
     logp, lse, ent, tl, ti = O.logprob(z, rp, ids, k)
     g = [None if t is None else to_np64(t) for t in out]
-    m = z.max(axis=1)
     row = np.repeat(np.arange(len(z)), np.diff(rp))
-    _near(g[0], logp, S + U * (np.abs(z[row, ids] - m[row]) + np.abs(logp)), "logp")
-    _near(g[1], lse, S + 2 * U * np.abs(lse), "lse")
+    m = z.max(axis=1)
+    zm = z[row, ids] - np.where(np.isfinite(m), m, 0)[row]
+    finite = np.isfinite(logp)
+    _near(g[0], logp, S + U * (np.abs(np.where(finite, zm, 0)) + np.abs(np.where(finite, logp, 0))), "logp")
+    _near(g[1], lse, S + 2 * U * np.abs(np.where(np.isfinite(lse), lse, 0)), "lse")
     _near(g[2], ent, 2 * S * (1 + ent), "entropy")
     if k:
         assert np.array_equal(g[4].astype(np.int64), ti), "alternatives"
@@ -69,3 +71,61 @@ def test_maximum_that_rises_far_from_zero(B, n_blocks, centre):
         for b in range(B):
             ids[4 * b:4 * b + 4].sort()
         _check(_run(zt, rp, ids, k), z, rp, ids, k)
+
+
+def _far_rows(N, dt, rng):
+    """Rows whose lse is too coarse to hold log S: of the type's lowest value, of that and
+    -inf, around +-70,000, 10^6, 10^30 and just beyond +-65,536."""
+    low = float(torch.finfo({"f32": torch.float32, "bf16": torch.bfloat16}[dt]).min)
+    half = rng.random(N) < 0.5
+    near = lambda c: c + rng.standard_normal(N) * 2 if dt == "f32" else np.where(half, c, c + 512)  # noqa: E731
+    rows = [np.full(N, low), np.where(half, low, -np.inf), near(70_000.0), near(-70_000.0), near(65_540.0), near(-65_600.0),
+            near(1e6), np.full(N, -1e30), np.where(half, 1e30, -1e30), np.full(N, -low), rng.standard_normal(N),
+            np.where(half, low, 1.0), np.where(half, -70_000.0, -np.inf)]
+    rows[-1][N // 2] = -70_000.0
+    return np.stack(rows)
+
+
+def _check_grad(got, z, rp, ids, g, gh, dt):
+    """p = e^((z - lse) - log S'), S' the row's sum of e^(z - lse): off by 2^-18 of itself for
+    the sum, u |z - lse| and u |log p| for the two differences and a few u for the
+    exponential; log p by the same amounts; the entropy by 2^-17 (1 + H); sums over a
+    list of m terms by m u; then half a step of the output type."""
+    ref = O.logprob_backward(z, rp, ids, g, gh)
+    _, _, Hr, _, _ = O.logprob(z, np.zeros(len(z) + 1, np.int64), [], 0)
+    m = z.max(axis=1)
+    lp = z - np.where(np.isfinite(m), m, 0.0)[:, None]
+    e = np.exp(lp)
+    p = e / np.where(e.sum(axis=1) > 0, e.sum(axis=1), 1.0)[:, None]
+    lp = np.where(p > 0, np.abs(np.log(np.where(p > 0, p, 1.0))), 0.0)
+    row = np.repeat(np.arange(len(z)), np.diff(rp))
+    G, Ga = np.zeros(len(z)), np.zeros(z.shape)
+    np.add.at(G, row, np.abs(g))
+    np.add.at(Ga, (row, ids), np.abs(g))
+    gha, Hc = np.abs(gh)[:, None], Hr[:, None]
+    m = 8 + int(np.diff(rp).max())
+    rel = S + U * (m + 4 * lp)
+    tol = (torch.finfo(torch.bfloat16 if dt == "bf16" else torch.float32).eps / 2 * np.abs(ref) + U * m * Ga
+           + 2 * rel * p * (G[:, None] + gha * (lp + Hc)) + p * gha * (rel + 2 * S * (1 + Hc)) + 1e-37)
+    _near(got, ref, tol, "d_logits")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 70, 1000, 2000, 9000, 70_001, 300_000])
+def test_gradient_where_lse_cannot_hold_the_sum(N, dt):
+    rng = np.random.default_rng(N)
+    r = _far_rows(N, dt, rng)
+    zt, z = _logits(r, dt, offset=N % 3)
+    rp, ids = _lists([min(3, N)] * len(r), N, rng)
+    g, gh = rng.standard_normal(len(ids)).astype(np.float32), rng.standard_normal(len(r)).astype(np.float32)
+    out = _run(zt, rp, ids, 0)
+    _check(out, z, rp, ids, 0)
+    _, lse, ent, _, _ = out
+    dev = lambda a: torch.as_tensor(a, device="cuda")  # noqa: E731
+    outs = []
+    for _ in range(2):
+        dz = torch.full_like(zt, 9.0)
+        H.haste_logprob_backward(zt, lse, ent, dev(rp), dev(ids), dev(g), dev(gh), dz)
+        outs.append(dz)
+    assert torch.equal(*outs)
+    _check_grad(to_np64(outs[0]), z, rp, ids, g, gh, dt)
