@@ -12,9 +12,11 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <thread>
+#include <utility>
 #include <vector>
 
 #include "head.cu"
@@ -1080,6 +1082,16 @@ static haste_status_t check_aligned(const void* p, size_t bytes, const char* nam
   return HASTE_OK;
 }
 
+// The softmax calls' lists, per-label and per-sample values, all of 4-byte elements (NULL
+// for what a call does not touch).
+static haste_status_t check_words(std::initializer_list<std::pair<const void*, const char*>> all) {
+  for (const auto& [p, name] : all) {
+    const haste_status_t st = check_aligned(p, 4, name);
+    if (st != HASTE_OK) return st;
+  }
+  return HASTE_OK;
+}
+
 int32_t haste_i8_pitch(int32_t n) { return n <= 0 || n > 0x7ffffff0 ? 0 : head8::pitch(n); }
 
 haste_status_t haste_quantize_rows(int64_t rows, int32_t n, haste_dtype_t dt, const void* x, int8_t* q, float* scale,
@@ -1195,6 +1207,11 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void*
   if (!logits || (nnz > 0 && !logp) || (k > 0 && (!top_logp || !top_id)))
     return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
   if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
+  if (nnz == 0) given = {nullptr, nullptr}, logp = nullptr;
+  if (k == 0) top_logp = nullptr, top_id = nullptr;
+  st = check_words({{given.row_ptr, "row_ptr"}, {given.ids, "ids"}, {logp, "logp"}, {lse, "lse"}, {entropy, "entropy"},
+                    {top_logp, "top_logp"}, {top_id, "top_id"}});
+  if (st != HASTE_OK) return st;
   const int n_run = (int)logprob::forward_runs(B, logprob_blocks(logits, N, dt), N * elem_bytes(dt));
   size_t keys;
   if ((st = check_ws(ws, ws_bytes, logprob_ws(B, N, dt, k, &keys))) != HASTE_OK) return st;
@@ -1205,7 +1222,7 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dt, const void*
   logprob::Args a{};
   a.logits = logits;
   a.N = N;
-  a.row_ptr = nnz > 0 ? given.row_ptr : nullptr;
+  a.row_ptr = given.row_ptr;
   a.ids = given.ids;
   a.nnz = nnz;
   a.k = k;
@@ -1240,6 +1257,11 @@ haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dt, co
   if (d_entropy && !entropy) return fail(HASTE_ERR_INVALID_ARG, "d_entropy needs the entropies");
   if ((st = check_aligned(logits, elem_bytes(dt), "logits")) != HASTE_OK) return st;
   if ((st = check_aligned(d_logits, elem_bytes(dt), "d_logits")) != HASTE_OK) return st;
+  if (nnz == 0) given = {nullptr, nullptr}, d_logp = nullptr;
+  if (!d_entropy) entropy = nullptr;
+  st = check_words({{lse, "lse"}, {entropy, "entropy"}, {given.row_ptr, "row_ptr"}, {given.ids, "ids"},
+                    {d_logp, "d_logp"}, {d_entropy, "d_entropy"}});
+  if (st != HASTE_OK) return st;
   const uintptr_t za = reinterpret_cast<uintptr_t>(logits), ga = reinterpret_cast<uintptr_t>(d_logits);
   const uintptr_t bytes = (uintptr_t)B * (uintptr_t)N * elem_bytes(dt);
   if (za < ga + bytes && ga < za + bytes)
@@ -1248,7 +1270,7 @@ haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dt, co
   if ((st = device_info(di)) != HASTE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n_run = (int)logprob::grad_runs(B, logprob_blocks(logits, N, dt));
-  logprob::GradArgs a{logits, N, n_run, lse, entropy, nnz > 0 ? given.row_ptr : nullptr, given.ids, nnz, d_logp, d_entropy,
+  logprob::GradArgs a{logits, N, n_run, lse, entropy, given.row_ptr, given.ids, nnz, d_logp, d_entropy,
                       d_logits};
   ProfScope ps("logprob_backward", s);
   const cudaError_t e =
