@@ -337,7 +337,8 @@ size_t haste_head_i8_workspace_size(int32_t B, int32_t H, int32_t d);
  *   Xh      device [B, d] in dtype;  Wq device int8 [H, haste_i8_pitch(d)],
  *   16-byte aligned, and w_scale device fp32 [H], from haste_quantize_rows
  *   logits  device [B, H] in out_dtype (fp32 logits keep what haste_logprob reads)
- * Supported: d <= 131072, B and H up to 2^30 with B * H up to 2^42. */
+ * Supported: d <= 131072, B and H up to 2^30 with ceil(H / 128) * ceil(B / 16) up
+ * to 2^30. */
 haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtype_t dtype, const void* Xh,
                                      const int8_t* Wq, const float* w_scale, haste_dtype_t out_dtype, void* logits,
                                      void* ws, size_t ws_bytes, haste_stream_t stream);

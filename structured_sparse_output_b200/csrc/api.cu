@@ -1126,7 +1126,7 @@ haste_status_t haste_head_forward_i8(int32_t B, int32_t H, int32_t d, haste_dtyp
   if (st == HASTE_OK) st = check_i8(d, out_dt);
   if (st != HASTE_OK) return st;
   if (B <= 0 || H <= 0 || d <= 0) return fail(HASTE_ERR_INVALID_ARG, "B, H and d must be positive");
-  if (B > head8::kMaxBH || H > head8::kMaxBH || head8::max_tiles(B, H) > 0x7fffffff)
+  if (B > head8::kMaxBH || H > head8::kMaxBH || head8::max_tiles(B, H) > head8::kMaxTiles)
     return fail(HASTE_ERR_UNSUPPORTED_SHAPE, "B=%d, H=%d: more tiles than 32-bit indices count", B, H);
   if (!Xh || !Wq || !w_scale || !logits) return fail(HASTE_ERR_INVALID_ARG, "NULL tensor pointer");
   if ((st = check_aligned(Xh, elem_bytes(dt), "Xh")) != HASTE_OK) return st;

@@ -196,6 +196,7 @@ constexpr int kML = 128;      // labels per tile
 constexpr int kKB = 128;      // K bytes per stage
 constexpr int kMaxStages = 8;
 constexpr int kMaxBH = 1 << 30;  // B and H: tile coordinates are 32-bit
+constexpr int kMaxTiles = 1 << 30;  // a tile's number and the next one's of its CTA fit 32 bits
 // Tiles of the narrowest form a batch of B can take.
 inline int64_t max_tiles(int64_t B, int64_t H) { return (H + kML - 1) / kML * ((B + 15) / 16); }
 

@@ -37,3 +37,20 @@ def test_addresses_that_a_call_does_not_touch_are_not_looked_at():
                  lambda: _grad(d_entropy=None, entropy=P + 1, d_logp=P + 2)):
         assert call() == ARG
         assert [w for w in (b"logits", b"row_ptr", b"lse", b"d_logp") if w in H.lib().haste_last_error()]
+
+
+def _head(B, Hh):
+    """The 8-bit head's status with a workspace of no bytes, so that no call gets to a device."""
+    return H.lib().haste_head_forward_i8(B, Hh, 64, H.HASTE_BF16, P, P, P, H.HASTE_F32, P, P, 0, None)
+
+
+@pytest.mark.parametrize("B,Hh", [(16 << 15, 128 << 15), (1, 1 << 30), (1 << 30, 1), (1 << 30, 2048), (2048, 1 << 30)])
+def test_head_i8_takes_up_to_2_30_tiles(B, Hh):
+    """Tile numbers count on by the number of CTAs beyond the last one, in 32 bits."""
+    assert _head(B, Hh) == H.HASTE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("B,Hh", [((16 << 15) + 1, 128 << 15), (16 << 15, (128 << 15) + 1), (4096, 1 << 30), (1 << 30, 2049),
+                                  ((1 << 31) // 2 + 1, 1), (16 << 16, (128 << 15) - 128)])
+def test_head_i8_refuses_more_than_2_30_tiles(B, Hh):
+    assert _head(B, Hh) == SHAPE
