@@ -231,20 +231,41 @@ __host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// 32 lanes x 32 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+// 32 lanes x kN consecutive columns of 32-bit integers, in flight until landed() is called
+// on them.
+template <int kN>
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, int (&r)[kN]) {
+  static_assert(kN == 8 || kN == 16 || kN == 32, "columns of one load");
+  if constexpr (kN == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+        "%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  } else if constexpr (kN == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  }
+}
+// Waits for the loads in flight.  The columns are passed on from behind the wait, so that no
+// use of them, a conversion in registers included, can be placed before it.
+template <int kN>
+__device__ __forceinline__ void landed(int (&r)[kN]) {
+  tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -270,26 +291,22 @@ __device__ __forceinline__ void store_tile(const Args& a, uint32_t src, int h, i
   const bool pairs = sizeof(O) == 2 && (a.H & 1) == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
   const bool all = h - lane + 32 <= a.H;
   const int n_c = min(kChunks, (a.B - b0 + CH - 1) / CH);
-  float v[2][CH];
-  auto fetch = [&](int c, float (&to)[CH]) {
-    if constexpr (CH == 32) tmem_ld32(src + (uint32_t)(c * CH), to);
-    else if constexpr (CH == 16) tmem_ld16(src + (uint32_t)(c * CH), to);
-    else tmem_ld8(src + (uint32_t)(c * CH), to);
-  };
-  if (n_c > 0) fetch(0, v[0]);
+  int v[2][CH];
+  if (n_c > 0) tmem_ld_async(src, v[0]);
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     if (c >= n_c) break;
-    tmem_wait_ld();
-    if (c + 1 < kChunks && c + 1 < n_c) fetch(c + 1, v[(c + 1) & 1]);
-    float(&z)[CH] = v[c & 1];
+    const int(&sum)[CH] = v[c & 1];
+    landed(v[c & 1]);
+    if (c + 1 < kChunks && c + 1 < n_c) tmem_ld_async(src + (uint32_t)((c + 1) * CH), v[(c + 1) & 1]);
+    float z[CH];
 #pragma unroll
     for (int i = 0; i < CH; i += 4) {
       const float4 sx = *reinterpret_cast<const float4*>(sxs + c * CH + i);
-      z[i] = (float)__float_as_int(z[i]) * (sx.x * sw);
-      z[i + 1] = (float)__float_as_int(z[i + 1]) * (sx.y * sw);
-      z[i + 2] = (float)__float_as_int(z[i + 2]) * (sx.z * sw);
-      z[i + 3] = (float)__float_as_int(z[i + 3]) * (sx.w * sw);
+      z[i] = (float)sum[i] * (sx.x * sw);
+      z[i + 1] = (float)sum[i + 1] * (sx.y * sw);
+      z[i + 2] = (float)sum[i + 2] * (sx.z * sw);
+      z[i + 3] = (float)sum[i + 3] * (sx.w * sw);
     }
     const int left = a.B - b0 - c * CH;  // samples from this column on
     O* row = out + (int64_t)(b0 + c * CH) * a.H + h;
