@@ -1036,58 +1036,72 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_logprob_rows(Args a, int B) 
   if (keep.n < a.k) fill_others(row, 0, a.N, keep.n, a.k, emit);
 }
 
-// Beyond kFar an fp32 lse is too coarse to hold log S (of a row of the type's lowest value it
-// holds nothing of it).  What it lacks is the log of the row's sum of e^(z - lse), which
-// the threads of a row's warp or of each of its CTAs take again: this is their part of it.
-__device__ __forceinline__ bool lacks(float lse) { return fabsf(lse) >= kFar && fabsf(lse) < INFINITY; }
+// The dense term of a row's gradient, by its definition: for single labels, and for rows
+// whose lse lies beyond kFar.  An fp32 lse is too coarse there to hold log S (of a row of
+// the type's lowest value it holds nothing of it); `lack` is what it lacks.
+struct Term {
+  float lse, H, gH, G, lack;
+  __device__ bool none() const { return lse == -INFINITY; }
+  __device__ bool near() const { return fabsf(lse) < kFar || lse != lse; }
+  __device__ float at(float v) const {
+    const float lp = (v - lse) - lack, p = ex2(lp * kLog2e);
+    return p == 0.f || none() ? 0.f : -p * fmaf(gH, lp + H, G);
+  }
+};
+// The terms of vectors [v0, v1) of a row beyond kFar (or of nothing but -inf), by the kStep
+// threads of the row's warp or of one of its CTAs; gives the row's `lack`, the log of its
+// sum of e^(z - lse), which they take over the whole row.
 template <typename T, int kStep>
-__device__ __noinline__ double far_sum(const Row<T> row, float lse) {
-  const uint32_t n_vec = (uint32_t)((row.N + (int64_t)row.head + Row<T>::kE - 1) / Row<T>::kE);
-  double S = 0.;
-  for (uint32_t v = threadIdx.x % kStep; v < n_vec; v += kStep) S += far_sums<T>(row.load(v), lse).x;
+__device__ __noinline__ float far_terms(const Row<T> row, T* dz, uint32_t v0, uint32_t v1, Term f) {
+  constexpr int kE = Row<T>::kE;
+  const uint32_t t = threadIdx.x % kStep, n_vec = (uint32_t)((row.N + (int64_t)row.head + kE - 1) / kE);
+  if (fabsf(f.lse) < INFINITY) {
+    double S = 0.;
+    for (uint32_t v = t; v < n_vec; v += kStep) S += far_sums<T>(row.load(v), f.lse).x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-  return S;
+    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    if constexpr (kStep > 32) {
+      __shared__ double part[kStep / 32];
+      if (t % 32 == 0) part[t / 32] = S;
+      __syncthreads();
+      S = 0.;
+      for (int i = 0; i < kStep / 32; ++i) S += part[i];
+    }
+    if (S > 0.) f.lack = logf((float)S);
+  }
+  for (uint32_t v = v0 + t; v < min(v1, n_vec); v += kStep) {
+    const int64_t j = row.column(v);
+    float z[kE];
+    unpack<T>(row.load(v), z);
+    for (int e = 0; e < kE; ++e)
+      if (j + e >= 0 && j + e < row.N) dz[j + e] = Elem<T>::from_f(f.at(z[e]));
+  }
+  return f.lack;
 }
-__device__ __forceinline__ float lack_of(double S) { return S > 0. ? logf((float)S) : 0.f; }
 
-// The dense term of a row's gradient.  With y = z log2(e) - R, R = fl(lse log2(e)) and
+// The same for vectors of a row within kFar.  With y = z log2(e) - R, R = fl(lse log2(e)) and
 // e = lse log2(e) - R, which an fma gives exactly, p = 2^(y - e) and log p = ln2 (y - e):
 // the term is -2^y (A + C y) with A and C of the row.
 template <typename T>
 struct Dense {
   static constexpr int kE = 16 / sizeof(T), kP = kE / 2;
-  float lse, lack, H, gH, G, lo;
-  bool none, near;
+  float lo;
   f2 R2, A2, C2;
-  __device__ Dense(float lse_, float lack_, float H_, float gH_, float G_)
-      : lse(lse_), lack(lack_), H(H_), gH(gH_), G(G_), lo(floor_of(lse_)), none(lse_ == -INFINITY),
-        near(fabsf(lse_) < kFar || lse_ != lse_) {
-    const float R = lse * kLog2e, e0 = fmaf(lse, kLog2e, -R), w = -ex2(-e0);
-    const float A = w * fmaf(gH, fmaf(-kLn2, e0, H), G), C = w * gH * kLn2;
+  __device__ explicit Dense(const Term& f) : lo(floor_of(f.lse)) {
+    const float R = f.lse * kLog2e, e0 = fmaf(f.lse, kLog2e, -R), w = -ex2(-e0);
+    const float A = w * fmaf(f.gH, fmaf(-kLn2, e0, f.H), f.G), C = w * f.gH * kLn2;
     R2 = pair(-R, -R);
     A2 = pair(A, A);
     C2 = pair(C, C);
   }
-  // the definition, for single labels and where R would lose too much
-  __device__ float at(float v) const {
-    const float lp = (v - lse) - lack, p = ex2(lp * kLog2e);
-    return p == 0.f || none ? 0.f : -p * fmaf(gH, lp + H, G);
-  }
   __device__ void of(const uint4& raw, float (&v)[kE]) const {
-    if (near) {
-      const f2 L2 = pair(kLog2e, kLog2e);
-      f2 x[kP];
-      raised<T>(raw, lo, x);
+    const f2 L2 = pair(kLog2e, kLog2e);
+    f2 x[kP];
+    raised<T>(raw, lo, x);
 #pragma unroll
-      for (int e = 0; e < kP; ++e) {
-        const f2 y = fma2(x[e], L2, R2);
-        unpair(mul2(ex2_2(y), fma2(y, C2, A2)), v[2 * e], v[2 * e + 1]);
-      }
-    } else {
-      unpack<T>(raw, v);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) v[e] = at(v[e]);
+    for (int e = 0; e < kP; ++e) {
+      const f2 y = fma2(x[e], L2, R2);
+      unpair(mul2(ex2_2(y), fma2(y, C2, A2)), v[2 * e], v[2 * e + 1]);
     }
   }
 };
@@ -1120,7 +1134,7 @@ __device__ __forceinline__ float list_sum(const GradArgs& a, int64_t p0, int64_t
 // by its thread: 256 x 8,192, 1,024 shuffled labels a row, 154 us against 8.7; in
 // ascending order 6.4.)
 template <typename T, int kStep, uint32_t kBits>
-__device__ __forceinline__ void put_given(const GradArgs& a, const Row<T>& row, T* dz, const Dense<T>& dense, int64_t p0,
+__device__ __forceinline__ void put_given(const GradArgs& a, const Row<T>& row, T* dz, const Term& term, int64_t p0,
                                           int64_t p1, int64_t c0, int64_t c1, bool ascending, uint32_t* once,
                                           uint32_t* again) {
   auto sync = [] {
@@ -1129,7 +1143,7 @@ __device__ __forceinline__ void put_given(const GradArgs& a, const Row<T>& row, 
   };
   const int t = threadIdx.x % kStep;
   sync();  // the dense term is written
-  auto put = [&](int64_t id, float g) { dz[id] = Elem<T>::from_f(g + dense.at(Elem<T>::to_f(row.z[id]))); };
+  auto put = [&](int64_t id, float g) { dz[id] = Elem<T>::from_f(g + term.at(Elem<T>::to_f(row.z[id]))); };
   if (ascending) {
     for (int64_t p = p0 + t; p < p1; p += kStep) {
       const int64_t id = a.ids[p];
@@ -1234,50 +1248,46 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
   } else {
     ascending = __all_sync(0xffffffffu, ascending);
   }
-  float lack = 0.f;
-  if (lacks(lse)) {
-    __shared__ double far_warp[kWarps];
-    double S = far_sum<T, kThreads>(row, lse);
-    if ((t & 31) == 0) far_warp[t >> 5] = S;
-    __syncthreads();
-    S = 0.;
-    for (int i = 0; i < kWarps; ++i) S += far_warp[i];
-    lack = lack_of(S);
-  }
-  const Dense<T> dense(lse, lack, H, gH, G);
-  // the output may sit on the 16-byte boundary differently from the input
-  const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
-  uint4* out_row = reinterpret_cast<uint4*>(dz - row.head) + t;
-  for (int blk = blk0; blk < blk1; ++blk) {
-    const bool more = blk + 1 < blk1, inside = blk + 1 >= in0 && blk + 1 < in1;
-    const bool whole = vec && blk >= in0 && blk < in1;
-    const uint32_t v0 = (uint32_t)blk * kBlock + t;
-    const uint4* next = at_row + (int64_t)(blk + 1) * kBlock;
-    uint4* out = out_row + (int64_t)blk * kBlock;
+  Term term{lse, H, gH, G, 0.f};
+  if (term.near()) {
+    const Dense<T> dense(term);
+    // the output may sit on the 16-byte boundary differently from the input
+    const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+    uint4* out_row = reinterpret_cast<uint4*>(dz - row.head) + t;
+    for (int blk = blk0; blk < blk1; ++blk) {
+      const bool more = blk + 1 < blk1, inside = blk + 1 >= in0 && blk + 1 < in1;
+      const bool whole = vec && blk >= in0 && blk < in1;
+      const uint32_t v0 = (uint32_t)blk * kBlock + t;
+      const uint4* next = at_row + (int64_t)(blk + 1) * kBlock;
+      uint4* out = out_row + (int64_t)blk * kBlock;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      float v[kE];
-      dense.of(raw[i], v);
-      if (more) raw[i] = inside ? next[i * kThreads] : row.load(v0 + kBlock + i * kThreads);
-      if (whole) {
-        out[i * kThreads] = packed<T>(v);
-      } else {
-        const int64_t j = row.column(v0 + i * kThreads);
+      for (int i = 0; i < kV; ++i) {
+        float v[kE];
+        dense.of(raw[i], v);
+        if (more) raw[i] = inside ? next[i * kThreads] : row.load(v0 + kBlock + i * kThreads);
+        if (whole) {
+          out[i * kThreads] = packed<T>(v);
+        } else {
+          const int64_t j = row.column(v0 + i * kThreads);
 #pragma unroll
-        for (int e = 0; e < kE; ++e)
-          if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
+          for (int e = 0; e < kE; ++e)
+            if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
+        }
       }
     }
+  } else {
+    term.lack = far_terms<T, kThreads>(row, dz, (uint32_t)blk0 * kBlock, (uint32_t)blk1 * kBlock, term);
   }
-  if (p0 == p1 || dense.none) return;
-  put_given<T, kThreads, kBits>(a, row, dz, dense, p0, p1, max(row.column((uint32_t)blk0 * kBlock), (int64_t)0),
+  if (p0 == p1 || term.none()) return;
+  put_given<T, kThreads, kBits>(a, row, dz, term, p0, p1, max(row.column((uint32_t)blk0 * kBlock), (int64_t)0),
                                 min(row.column((uint32_t)blk1 * kBlock), a.N), ascending, once, again);
 }
 
 // A warp per row, its kN vectors a lane in registers: 20,000 x 1,000 bf16 in 15.6 us, 5.1
-// TB/s read and written.
+// TB/s read and written.  4, 7 or 8 CTAs an SM (4,000 x 2,000 f32 with entropies, 16 vectors a
+// lane: 15.5 us against 17.4 without that bound on the registers).
 template <typename T, int kN>
-__global__ void __launch_bounds__(32 * kRowWarps) k_logprob_grad_rows(GradArgs a, int B) {
+__global__ void __launch_bounds__(32 * kRowWarps, kN == 16 ? 4 : kN == 8 ? 7 : 8) k_logprob_grad_rows(GradArgs a, int B) {
   constexpr int kE = 16 / sizeof(T);
   constexpr uint32_t kBits = 32 * kN * kE;  // one for each label
   __shared__ uint32_t once[kRowWarps][kBits / 32], again[kRowWarps][kBits / 32];
@@ -1298,23 +1308,28 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_logprob_grad_rows(GradArgs a
   bool ascending;
   const float G = list_sum(a, p0, p1, lane, 32, ascending);
   ascending = __all_sync(0xffffffffu, ascending);
-  const Dense<T> dense(lse, lacks(lse) ? lack_of(far_sum<T, 32>(row, lse)) : 0.f, H, gH, G);
-  const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+  Term term{lse, H, gH, G, 0.f};
+  if (term.near()) {
+    const Dense<T> dense(term);
+    const bool vec = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int64_t j = row.column(i * 32 + lane);
-    float v[kE];
-    dense.of(raw[i], v);
-    if (vec && row.whole(j)) {
-      *reinterpret_cast<uint4*>(dz + j) = packed<T>(v);
-    } else if (j < a.N) {
+    for (int i = 0; i < kN; ++i) {
+      const int64_t j = row.column(i * 32 + lane);
+      float v[kE];
+      dense.of(raw[i], v);
+      if (vec && row.whole(j)) {
+        *reinterpret_cast<uint4*>(dz + j) = packed<T>(v);
+      } else if (j < a.N) {
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
+        for (int e = 0; e < kE; ++e)
+          if (j + e >= 0 && j + e < a.N) dz[j + e] = Elem<T>::from_f(v[e]);
+      }
     }
+  } else {
+    term.lack = far_terms<T, 32>(row, dz, 0, ~0u, term);
   }
-  if (p0 == p1 || dense.none) return;
-  put_given<T, 32, kBits>(a, row, dz, dense, p0, p1, 0, a.N, ascending, once[w], again[w]);
+  if (p0 == p1 || term.none()) return;
+  put_given<T, 32, kBits>(a, row, dz, term, p0, p1, 0, a.N, ascending, once[w], again[w]);
 }
 
 // Blocks that a row of N elements can touch: of logits at this address, or (NULL)
