@@ -1,9 +1,11 @@
 """Builds libhaste.so (sm_100a) in-tree with nvcc, and with g++ the Python binding's
-native argument checks, _native.so.
+native argument checks, _native.<torch and Python version>.so.
 
 The library is one translation unit (api.cu includes the kernel sources), linked
-against the static CUDA runtime so that it depends only on the driver.  _native.so
-reads torch's tensors; it is loaded after torch, whose libraries it needs.
+against the static CUDA runtime so that it depends only on the driver.  The argument
+checks read torch's tensors by the layout of the headers that they were built with, so
+their file is named after the torch, its C++ ABI and the interpreter that it is for; it is
+loaded after torch, whose libraries it needs.
 """
 import os
 import subprocess
@@ -38,15 +40,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return OUT
 
 
-NATIVE_OUT = os.path.join(PKG, "_native.so")
 NATIVE_SOURCES = [os.path.join(HERE, "native.cpp"), os.path.join(HERE, "..", "..", "include", "haste.h")]
 
 
+def native_path() -> str:
+    """Where the argument checks for this torch and this interpreter are, or will be, built."""
+    import torch
+    tag = f"torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}-{sys.implementation.cache_tag}"
+    return os.path.join(PKG, f"_native.{tag}.so")
+
+
 def build_native(force: bool = False) -> str:
-    if not force and os.path.exists(NATIVE_OUT):
-        t = os.path.getmtime(NATIVE_OUT)
+    out = native_path()
+    if not force and os.path.exists(out):
+        t = os.path.getmtime(out)
         if all(os.path.getmtime(s) <= t for s in NATIVE_SOURCES):
-            return NATIVE_OUT
+            return out
     import sysconfig
 
     import torch
@@ -54,14 +63,14 @@ def build_native(force: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(NVCC))
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    tmp = NATIVE_OUT + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     subprocess.check_call(
         [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-o", tmp, NATIVE_SOURCES[0],
          *(a for i in include for a in ("-isystem", i)),
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L" + os.path.join(root, "lib"),
          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], cwd=HERE)
-    os.replace(tmp, NATIVE_OUT)
-    return NATIVE_OUT
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Optional, Tuple
 
 import numpy as np
@@ -416,22 +417,37 @@ def haste_head_backward(Xh, Wh, dYh, dWh, dXh, ws, stream=None) -> None:
                                      _tptr(dXh), p, n, _stream(stream)), "haste_head_backward")
 
 
+class _PythonChecks:
+    """In place of the C++ checks where they are not built: leaves every call to Python."""
+    logprob = logprob_backward = head_forward_i8 = staticmethod(lambda *args: None)
+
+
 _native_module = None
 
 
 def _native():
-    """The calls below with their checks made in C++ (built in-tree, like the library):
-    each returns the status, or None where a check does not hold."""
+    """The calls below with their checks made in C++ (built in-tree, like the library, for
+    one torch and one interpreter): each returns the status, or None where a check does not
+    hold.  Without that binary the Python checks below make the same calls, in some 6 us more."""
     global _native_module
     if _native_module is None:
+        from importlib import machinery, util
+
         import torch  # noqa: F401  (its libraries must be loaded first)
+
+        from .csrc import build
         L = lib()
+        path = build.native_path()
         try:
-            from . import _native as m
+            loader = machinery.ExtensionFileLoader(__package__ + "._native", path)
+            m = util.module_from_spec(util.spec_from_file_location(loader.name, path, loader=loader))
+            loader.exec_module(m)
+            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                     for f in (L.haste_logprob, L.haste_logprob_backward, L.haste_head_forward_i8)))
         except ImportError as e:
-            raise RuntimeError(f"_native.so is not built; run `python {os.path.join(_HERE, 'csrc', 'build.py')}`") from e
-        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                 for f in (L.haste_logprob, L.haste_logprob_backward, L.haste_head_forward_i8)))
+            warnings.warn(f"argument checks in C++ not loaded ({e}); the Python ones are used. Build them with "
+                          f"`python {os.path.join(_HERE, 'csrc', 'build.py')}`", RuntimeWarning, stacklevel=3)
+            m = _PythonChecks
         _native_module = m
     return _native_module
 
