@@ -93,8 +93,10 @@ haste_status_t device_info(DeviceInfo& di) {
   if (dev >= 0 && dev < kKnown) {
     static std::mutex mu;
     std::lock_guard<std::mutex> g(mu);
-    known[dev] = di;
-    is_known[dev].store(true, std::memory_order_release);
+    if (!is_known[dev].load(std::memory_order_relaxed)) {  // written once: others read it without the lock
+      known[dev] = di;
+      is_known[dev].store(true, std::memory_order_release);
+    }
   }
   return HASTE_OK;
 }
