@@ -129,3 +129,32 @@ def test_gradient_where_lse_cannot_hold_the_sum(N, dt):
         outs.append(dz)
     assert torch.equal(*outs)
     _check_grad(to_np64(outs[0]), z, rp, ids, g, gh, dt)
+
+
+@pytest.mark.parametrize("N", [2 ** 31 - 1, 2 ** 31 - 9])
+def test_longest_row(N):
+    """One bf16 row of as many labels as there are ids: the sums, the alternatives and the
+    gradient at both ends and past 2^30, by closed forms."""
+    z = torch.full((1, N), float("-inf"), dtype=torch.bfloat16, device="cuda")
+    at = [0, 5, 2 ** 30 - 1, 2 ** 30, N - 2, N - 1]
+    v = torch.tensor([1.0, 0.0, 2.0, 0.5, 2.0, 1.0])
+    z[0, torch.tensor(at, device="cuda")] = v.bfloat16().cuda()
+    p = torch.softmax(v.double(), 0)
+    lp = torch.log_softmax(v.double(), 0)
+    ids = np.array([N - 1, 7, 2 ** 30, 0], np.int32)
+    rp = np.array([0, 4], np.int32)
+    logp, lse, ent, tl, ti = _run(z, rp, ids, 8)
+    assert abs(lse.item() - torch.logsumexp(v.double(), 0).item()) < 2 * S
+    assert abs(ent.item() + (p * lp).sum().item()) < 4 * S
+    assert np.allclose(logp.cpu(), [lp[5], -np.inf, lp[3], lp[0]], atol=2 * S)
+    assert ti[0].tolist() == [2 ** 30 - 1, N - 2, 0, N - 1, 2 ** 30, 5, 1, 2]
+    assert np.allclose(tl[0, :6].cpu(), lp[[2, 4, 0, 5, 3, 1]], atol=2 * S) and (tl[0, 6:] == -np.inf).all()
+    dz = torch.empty_like(z)
+    dev = lambda a: torch.as_tensor(a, device="cuda")  # noqa: E731
+    H.haste_logprob_backward(z, lse, None, dev(rp), dev(ids), dev(np.array([3, 5, 2, 1], np.float32)), None, dz)
+    want = -11 * p
+    want[5] += 3
+    want[3] += 2
+    want[0] += 1
+    assert np.allclose(dz[0, torch.tensor(at, device="cuda")].double().cpu(), want, rtol=2.0 ** -8 + 2.0 ** -16)
+    assert dz[0, 7].item() == 5.0 and sum((c != 0).sum().item() for c in dz[0].split(2 ** 28)) == 7
