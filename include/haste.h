@@ -332,8 +332,10 @@ size_t haste_head_i8_workspace_size(int32_t B, int32_t H, int32_t d);
 /* Dense head logits from 8-bit weights, for scoring: the rows of Xh are quantised
  * (as haste_quantize_rows) within the call, and
  *   logits[b, h] = (float)(sum_f qx[b, f] * Wq[h, f]) * (sx[b] * w_scale[h]),
- * the sum exact in 32-bit integers on the tensor cores, the logits rounded to
- * out_dtype.  A sample with a NaN or an infinity gets NaN logits.
+ * the sum exact in 32-bit integers on the tensor cores (few samples: on the CUDA
+ * cores), the logits rounded to out_dtype.  The scales' product rounds to fp32 first:
+ * where it overflows (|x| |w| beyond about 5e42) a logit is infinite, or NaN for a
+ * sum of 0.  A sample with a NaN or an infinity gets NaN logits.
  *   Xh      device [B, d] in dtype;  Wq device int8 [H, haste_i8_pitch(d)],
  *   16-byte aligned, and w_scale device fp32 [H], from haste_quantize_rows
  *   logits  device [B, H] in out_dtype (fp32 logits keep what haste_logprob reads)
@@ -356,14 +358,17 @@ size_t haste_logprob_workspace_size(int32_t B, int64_t N, haste_dtype_t dtype, i
  *   entropy[b] = -sum_j p[b, j] log p[b, j];
  *   top_id [B, k], top_logp [B, k]: the k labels of the largest logits and their
  *   log p, larger logit first, equal logits by smaller label id.
- * All sums are held in fp32.  A masked label has the logit -inf: p = 0, log p =
+ * All sums are held in fp32; for rows of up to 2^20 labels they are off by less than
+ * 2^-18 of themselves wherever the logits lie, which log p and entropy show as an
+ * absolute 2^-18 beside their own roundings.  A masked label has the logit -inf: p = 0, log p =
  * -inf, no entropy.  A row of nothing but -inf has lse = log p = -inf and entropy
  * 0; a row with a NaN or +inf gets NaN throughout (its top_id ranks a NaN as -inf).
  *   logits    device [B, N] in dtype, contiguous
  *   given     row_ptr [B + 1] and ids [nnz]; unlike elsewhere the ids of a row may
  *             come in any order and repeat, and an id outside [0, N) gets NaN.
- *             row_ptr NULL: none (ids and logp are not read).  Entries of row_ptr
- *             are kept within [0, nnz]; logp [nnz] outside them is left as it was.
+ *             nnz = 0: none (row_ptr, ids and logp are not touched and may be
+ *             NULL).  Entries of row_ptr are kept within [0, nnz]; logp [nnz] outside
+ *             them is left as it was.
  *   lse, entropy  fp32 [B], each may be NULL;  logp fp32 [nnz]
  *   k         0 <= k <= min(64, N); top_logp and top_id may be NULL when k = 0
  * Supported: 1 <= N < 2^31.  The paper names no loss; the softmax reading, next to
@@ -383,9 +388,11 @@ haste_status_t haste_logprob(int32_t B, int64_t N, haste_dtype_t dtype, const vo
  * 1 / N).  Masked labels get 0
  * (and their own d_logp where they are given); rows of nothing but -inf get 0;
  * ids outside [0, N) count for nothing.  The choice of alternatives (top_*) has no
- * gradient.  The sums run in the order of the lists: repeats give the same bits.
- *   given.row_ptr NULL: no logp term.  d_entropy NULL: no entropy term (entropy is
- *   not read).  d_logits must not overlap logits. */
+ * gradient.  A label given several times is summed in the order of its list, G in a
+ * fixed order that goes by B, N and the list's length: equal calls give equal bits.
+ *   nnz = 0: no logp term (given and d_logp are not touched and may be NULL).
+ *   d_entropy NULL: no entropy term (entropy is not read).  d_logits must not
+ *   overlap logits. */
 haste_status_t haste_logprob_backward(int32_t B, int64_t N, haste_dtype_t dtype, const void* logits,
                                       const float* lse, const float* entropy, haste_targets_t given, int64_t nnz,
                                       const float* d_logp, const float* d_entropy, void* d_logits,

@@ -4,6 +4,10 @@
 // s = max|x| / 127 rounded once to fp32, q = the exact quotient x / s rounded half
 // to even.  Product: z[b, h] = (float)(sum_f qx[b, f] qw[h, f]) * (sx[b] * sw[h]),
 // the sum exact in 32 bits (tcgen05 kind::i8).
+//
+// Times in this file are of one call among others in a CUDA graph on the same inputs; a
+// program's calls one by one take longer at the largest size (512 x 131,072 x 1024: 90 us
+// where 76 stand here).
 #include "common.cuh"
 #include "launch.cuh"
 
@@ -32,8 +36,9 @@ __device__ __forceinline__ int quantise(float x, float s) {
 // number in the low bits of the sum, inv being 1 / s to an ulp; the exact remainder
 // then moves a quotient that fell on the wrong side of a half (half the row's maximum
 // lies next to 63.5, and bf16 rows meet it often).  Scales too small for a reciprocal
-// (inv = 0) take the division above.  (Divisions throughout took 249 us for 131,072
-// rows of 1,024 bf16 values, and 4 us for a single one.)
+// (inv = 0) take the division above.  131,072 rows of 1,024 bf16 values take 140 us (their
+// bytes 61 at a copy's rate; the corrections' instructions bound it), 256 of 768 1.9 us.
+// (Divisions throughout took 249 us, and 4 us for a single row.)
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, float inv) {
   constexpr float kM = 12582912.f;
   uint32_t b[8];
@@ -186,7 +191,7 @@ cudaError_t launch_quantize(int64_t rows, int n, const void* x, int8_t* q, float
 //              TMEM accumulators of BN columns
 //   warps 2-9  epilogue: warp (q, half) reads lane quarter q of its half of the
 //              columns, scales and stores
-// 512 x 131,072 x 1024 to bf16: 74 us, 1.86 Pop/s, against 41 us for its bytes at a
+// 512 x 131,072 x 1024 to bf16: 76 us, 1.8 Pop/s, against 41 us for its bytes at a
 // copy's rate.  The MMAs alone take 49 us (199 clocks for 128 x 256 x 32), the whole
 // without loads 65 and without the epilogue 58: staging 48 KB for 4 MMAs, the MMAs and
 // the epilogue's TMEM reads share an SM's ports.  Up to some hundred samples the
@@ -611,7 +616,9 @@ cudaError_t launch_product_t(Args a, int ld, const int8_t* qx, const int8_t* qw,
 
 // Where the tiles are slower: up to 16,384 labels (two launches against one), and one
 // or two samples of rows long enough to occupy a warp's lanes (1 x 131,072 x 1024 22.8
-// and 28.1 us, but x 256 13.6 and 10.4 us).  Three and four samples of more than 1,024
+// and 28.1 us, but x 256 11.9 and 10.1 us).  In between the two forms change places where
+// the rule does not (x 512 13.6 and 15.3 us for one sample, 16.6 and 15.3 for two; x 768 18.5
+// and 22.3, 21.7 and 22.5).  Three and four samples of more than 1,024
 // features take as long as the tiles, or longer (4 x 16,384 x 4096: 24 and 18 us).
 inline int few_samples(int B) { return B <= 2 ? B : 4; }
 inline bool few(int B, int H, int ld) {

@@ -7,6 +7,10 @@
 // join by rescaling S and T to the common maximum.
 // Rank order of the alternatives: larger logit first, equal logits by smaller id.
 // Gradient: dz_j = sum_{i: id_i = j} g_i - p_j (sum_i g_i + gH (log p_j + entropy)).
+//
+// Times in this file are of one call among others in a CUDA graph on the same inputs, those
+// of less than about 60 MB in L2; a program's calls one by one take up to 7 % longer at the
+// largest sizes (256 x 670,208: 76 us where 70 stand here, the gradient 117 for 110).
 #include <cfloat>
 
 #include "common.cuh"
@@ -1131,8 +1135,9 @@ __device__ __forceinline__ float list_sum(const GradArgs& a, int64_t p0, int64_t
 // written.  In a list that ascends each label is given once.  In any other a label that
 // may be given again (it shares its bit of `again` with a second entry) is looked for in
 // the whole list by its warp, and its first entry takes the sum.  (Every label looked for
-// by its thread: 256 x 8,192, 1,024 shuffled labels a row, 154 us against 8.7; in
-// ascending order 6.4.)
+// by its thread: 256 x 8,192, 1,024 shuffled labels a row, 154 us against 8.3; in
+// ascending order 6.0.  Lists of many repeats are slower for it: 256 rows of 50 labels
+// given 400 times 77 us, 9,000 labels 68, against 33.)
 template <typename T, int kStep, uint32_t kBits>
 __device__ __forceinline__ void put_given(const GradArgs& a, const Row<T>& row, T* dz, const Term& term, int64_t p0,
                                           int64_t p1, int64_t c0, int64_t c1, bool ascending, uint32_t* once,
@@ -1209,7 +1214,7 @@ __device__ __forceinline__ void put_given(const GradArgs& a, const Row<T>& row, 
 }
 
 // One CTA per run of a row: the dense term of its blocks, then the given labels in
-// them.  Bound by memory: 256 x 670,208 bf16 in 109 us, 6.3 TB/s read and written, 96%
+// them.  Bound by memory: 256 x 670,208 bf16 in 110 us, 6.2 TB/s read and written, 95%
 // of a copy's rate.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
@@ -1283,8 +1288,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprob_grad(GradArgs a) {
                                 min(row.column((uint32_t)blk1 * kBlock), a.N), ascending, once, again);
 }
 
-// A warp per row, its kN vectors a lane in registers: 20,000 x 1,000 bf16 in 15.6 us, 5.1
-// TB/s read and written.  4, 7 or 8 CTAs an SM (4,000 x 2,000 f32 with entropies, 16 vectors a
+// A warp per row, its kN vectors a lane in registers: 20,000 x 1,000 bf16 in 14.9 us, 5.4
+// TB/s read and written (21 us, 3.8 TB/s, from and to HBM).  4, 7 or 8 CTAs an SM (4,000 x 2,000 f32 with entropies, 16 vectors a
 // lane: 15.5 us against 17.4 without that bound on the registers).
 template <typename T, int kN>
 __global__ void __launch_bounds__(32 * kRowWarps, kN == 16 ? 4 : kN == 8 ? 7 : 8) k_logprob_grad_rows(GradArgs a, int B) {
@@ -1349,11 +1354,13 @@ inline int64_t runs(int B, int64_t blocks, int64_t ctas, int64_t least) {
 // Whole rows where that leaves the SMs busy or a row is short: the start of a run
 // and the join cost as much as several blocks.  Measured with 5 alternatives, whole
 // against split: 256 x 65,536 bf16 13.1 and 20.4 us, 256 x 131,072 20.1 and 25.2 us,
-// 64 x 32,003 8.7 and 9.4 us; but 1 x 65,536 9.6 and 6.9 us, 256 x 670,208 (4 runs)
-// 87 and 73 us.
+// 64 x 40,000 8.2 and 10.5 us, 64 x 65,536 9.9 and 10.7 us, 100 x 65,536 10.2 and 12.5
+// us; but 1 x 65,536 9.6 and 6.9 us, 256 x 670,208 (4 runs) 87 and 73 us.
 // One block a run (the last half a block to one and a half, so that none is empty
-// wherever the rows start) where that leaves no more CTAs than SMs: 8 x 65,536 bf16 7.2 us with 5 alternatives, 10.0 with 64, against 8.5 and 11.4 in
-// runs of two.
+// wherever the rows start) where that leaves no more CTAs than SMs: 8 x 65,536 bf16 7.2
+// us with 5 alternatives, 10.0 with 64, against 8.5 and 11.4 in runs of two.
+// The numbers of CTAs (888 and 3,552 are six and 24 a SM) are a B200's and not the device's:
+// the workspace's size follows from them, and a host without a GPU may ask for it.
 constexpr int64_t kSpread = 148;
 inline int64_t forward_runs(int B, int64_t blocks, int64_t row_bytes) {
   if (blocks <= 4 || (B >= 64 && blocks <= 8) || (B >= 128 && blocks <= 16)) return 1;
@@ -1406,8 +1413,8 @@ cudaError_t launch_join(int B, const Args& a, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t launch_grad(int B, const GradArgs& a, cudaStream_t st) {
-  // a warp a row: 1 x 1,000 bf16 in 3.0 us (3.7 by a CTA), 20,000 x 1,000 in 15.6 (154),
-  // 256 x 2,000 fp32 in 5.3 (4.1), 2,048 x 2,000 in 7.6 (14.4)
+  // a warp a row: 1 x 1,000 bf16 in 2.5 us (3.3 by a CTA), 20,000 x 1,000 in 14.9 (152);
+  // 1 x 2,000 fp32 in 3.4 (2.9), 256 x 2,000 in 3.9 (3.9), 512 x 2,000 in 3.9 (5.4)
   const int vecs = lane_vectors<T>(a.logits, a.N);
   const unsigned grid = (unsigned)((B + (int64_t)kRowWarps - 1) / kRowWarps);
   if (vecs == 4) return launch_early(k_logprob_grad_rows<T, 4>, grid, 32 * kRowWarps, 0, st, a, B);
